@@ -128,6 +128,43 @@ moe_status moe_router_logits(const void* x, moe_dtype xt, const float* w_router,
 moe_status moe_route(const float* logits, int T, int E, int k, int32_t* ids, float* w,
                      moe_stream_t stream);
 
+/* Expert choice by scores, a balance bias and groups of experts.  Per token,
+ * in double precision from logits l:
+ *   score   s[e] = softmax over all E of l (MOE_SCORE_SOFTMAX), or
+ *                  1 / (1 + exp(-l[e])) (MOE_SCORE_SIGMOID)
+ *   choice  c[e] = s[e] + bias[e] (bias NULL: s[e]); the bias steers the choice
+ *           and never enters a weight
+ *   groups  of E / groups consecutive experts; a group's value is its best c
+ *           (MOE_GROUP_MAX) or the sum of its two best (MOE_GROUP_TOP2); the
+ *           topk_groups best groups stay, ties to the lower group
+ *   picks   the k best c of those groups, ties to the lower expert
+ *   weight  w = s of the pick, divided by the picks' sum if renorm, times scale
+ * Picks come out with falling s, ties to the lower expert: the rank order that
+ * the precision ladder and moe_combine expect.
+ * Masked experts: a logit of NaN, -inf or a type's lowest value (anything down
+ * from bf16's, -0x1.fep127), or a choice of -inf or NaN.  They
+ * count in no group's value (a group of masked experts alone is worth -inf) and
+ * are picked, lower ids first, only where the chosen groups hold fewer than k
+ * others; their weight is 0.  Logits of +inf share a softmax equally.  A sum of
+ * 0 renormalises to weights of 0. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+
+typedef struct {
+  int E, k;            /* 1 <= k <= E <= 1024, k <= 64 */
+  int scoring;         /* MOE_SCORE_* */
+  int groups;          /* divides E, <= 64; 1 = no groups */
+  int topk_groups;     /* 1..groups, topk_groups * E / groups >= k */
+  int group_score;     /* MOE_GROUP_* */
+  int renorm;          /* 0 or 1 */
+  float scale;         /* finite */
+} moe_router;
+
+/*   logits [T][E] in lt (MOE_F32 or MOE_BF16), bias [E] fp32 or NULL,
+ *   ids [T][k] int32 out, w [T][k] fp32 out.  0 <= T <= 2^20 (0: no launch). */
+moe_status moe_route_groups(const moe_router* router, const void* logits, moe_dtype lt, const float* bias, int T,
+                            int32_t* ids, float* w, moe_stream_t stream);
+
 /* Stable grouping of n keys in [0, nkeys): counts [nkeys], offsets [nkeys+1]
  * (exclusive prefix of counts), perm [n] = indices of the keys sorted by key,
  * ascending index within a key.  Used to group the (token, rank) pairs by
@@ -148,6 +185,71 @@ moe_status moe_group(const int32_t* keys, int n, int nkeys, int32_t* counts, int
 size_t moe_group_scratch_bytes(int n, int nkeys);
 moe_status moe_group_wide(const int32_t* keys, int n, int nkeys, int32_t* counts, int32_t* offsets,
                           int32_t* perm, void* scratch, moe_stream_t stream);
+
+/* ------------------------------------------------------------ around the block */
+
+/* RMS norms before and after a block, with the gate and the scale on its way
+ * back into the residual stream.  RMS(z; w) = z / sqrt(mean(z^2) + eps) * (weight_offset + w),
+ * a NULL weight: times 1.  Sums and arithmetic in fp32 (a row whose sum of
+ * squares passes fp32's range norms to 0), one rounding per output. */
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 };  /* none, [H], [T], [T][H] */
+enum { MOE_GATE_LINEAR = 0, MOE_GATE_SIGMOID = 1 };  /* the gate as it is, or 1 / (1 + exp(-gate)) */
+
+typedef struct {
+  int H;               /* 1..16384 */
+  float eps;           /* >= 0 */
+  float weight_offset; /* 0 where weights are stored as they act, 1 where around zero */
+  moe_dtype wt;        /* type of pre_w and post_w */
+  const void* pre_w;   /* [H] weight of the norm before the block, or NULL */
+  const void* post_w;  /* [H] weight of the norm after the block, or NULL */
+  int post_norm;       /* 1: the block's output is normed; 0: taken as it is */
+  int gate;            /* MOE_GATE_NONE .. MOE_GATE_FULL */
+  int gate_act;        /* MOE_GATE_LINEAR or MOE_GATE_SIGMOID */
+  float alpha;         /* residual scale */
+} moe_norm;
+
+/* The norm before the block: out[t] = RMS(x[t]; pre_w).
+ *   x [T][H] in xt, out [T][H] in ot; out may be x where xt == ot.
+ * 0 <= T <= 2^20 (0: no launch).  Pointers aligned to their element. */
+moe_status moe_norm_in(const moe_norm* norm, const void* x, moe_dtype xt, int T, void* out, moe_dtype ot,
+                       moe_stream_t stream);
+
+/* The way back into the stream, and the next block's norm in the same pass:
+ *     z        = RMS(y[t]; post_w) (post_norm) or y[t]
+ *     r        = residual[t] + alpha * act(gate) * z
+ *     out[t]   = r
+ *     next_out[t] = RMS(r; next->pre_w), of r before it is rounded to out's type
+ *   y [T][H] in yt, residual and out [T][H] in rt, gate in gt (NULL with
+ *   MOE_GATE_NONE), next_out [T][H] in nt; next and next_out both NULL: not
+ *   computed.  next->H == norm->H.  out and next_out may each be the buffer of y
+ *   or residual where the types are equal, and must differ from each other. */
+moe_status moe_norm_out(const moe_norm* norm, const void* y, moe_dtype yt, const void* residual, const void* gate,
+                        moe_dtype gt, int T, void* out, moe_dtype rt, const moe_norm* next, void* next_out,
+                        moe_dtype nt, moe_stream_t stream);
+
+/* Low-rank adapters of many requests beside a projection that all of them
+ * share (FP4 weights cannot take an adapter in without being quantised again):
+ *     out[t] = base[t] + scale[a] * B[a] (A[a] x[t]),   a = adapter_ids[t]
+ * Only the first min(ranks[a], r) rows of A[a] and columns of B[a] count.  A
+ * token whose id is outside [0, num) has no adapter: out[t] = base[t].  No
+ * token's result depends on another's adapter.  fp32 sums, one rounding.
+ * Requests' tokens may stand in any order; long batches run best where a
+ * request's tokens stand together. */
+typedef struct {
+  int K, N;              /* inputs and outputs of the projection, 1..65536 */
+  int r;                 /* rank the bank is laid out for, 1..128 */
+  int num;               /* adapters in the bank, 0..65536 */
+  const void* a;         /* [num][r][K] bf16 */
+  const void* b;         /* [num][N][r] bf16 */
+  const float* scale;    /* [num], or NULL (all 1) */
+  const int32_t* ranks;  /* [num], or NULL (all r) */
+} moe_lora;
+
+/*   x [T][K] in xt, adapter_ids [T] int32, base [T][N] in yt or NULL (zeros),
+ *   out [T][N] in yt; out may be base.  0 <= T <= 2^20 (0: no launch).  a and b
+ *   2-byte, the others element aligned (16-byte: wide loads). */
+moe_status moe_lora_add(const moe_lora* lora, const void* x, moe_dtype xt, int T, const int32_t* adapter_ids,
+                        const void* base, void* out, moe_dtype yt, moe_stream_t stream);
 
 /* ------------------------------------------------------------ expert MLP */
 
@@ -475,7 +577,9 @@ typedef enum {
   MOE_PROF_CACHE = 12,      /* slot cache: picks to the host, rewritten ids back */
   MOE_PROF_FUSED = 13,      /* fused batch-1 step: routing, gate/up, down and combine in one launch */
   MOE_PROF_SCRATCH = 14,    /* one-time clear of the static scratch (moe_layer_decode_noalloc) */
-  MOE_PROF_KINDS = 16
+  MOE_PROF_NORM = 15,       /* norms around the block */
+  MOE_PROF_LORA = 16,       /* requests' adapters */
+  MOE_PROF_KINDS = 24
 } moe_prof_kind;
 
 /* Start timing the library's kernels: every launch made after this call is

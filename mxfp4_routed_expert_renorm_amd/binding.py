@@ -62,6 +62,34 @@ class moe_cache_stats(ctypes.Structure):
     ]
 
 
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+GATE_LINEAR, GATE_SIGMOID = 0, 1
+
+
+class moe_router(ctypes.Structure):
+    _fields_ = [
+        ("E", c_int), ("k", c_int), ("scoring", c_int), ("groups", c_int), ("topk_groups", c_int),
+        ("group_score", c_int), ("renorm", c_int), ("scale", ctypes.c_float),
+    ]
+
+
+class moe_norm(ctypes.Structure):
+    _fields_ = [
+        ("H", c_int), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("wt", c_int),
+        ("pre_w", c_void_p), ("post_w", c_void_p), ("post_norm", c_int), ("gate", c_int), ("gate_act", c_int),
+        ("alpha", ctypes.c_float),
+    ]
+
+
+class moe_lora(ctypes.Structure):
+    _fields_ = [
+        ("K", c_int), ("N", c_int), ("r", c_int), ("num", c_int),
+        ("a", c_void_p), ("b", c_void_p), ("scale", c_void_p), ("ranks", c_void_p),
+    ]
+
+
 _SIGS = {
     "moe_last_error": (c_char_p, []),
     "moe_version": (c_char_p, []),
@@ -69,6 +97,11 @@ _SIGS = {
     "moe_int2_expert_bytes": (c_size_t, [c_int, c_int]),
     "moe_router_logits": (c_int, [c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p]),
     "moe_route": (c_int, [c_void_p, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p]),
+    "moe_route_groups": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
+    "moe_norm_in": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_int, c_void_p]),
+    "moe_norm_out": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_int, c_int, c_void_p, c_int, c_void_p,
+                             c_void_p, c_int, c_void_p]),
+    "moe_lora_add": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_int, c_void_p]),
     "moe_group": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p]),
     "moe_group_scratch_bytes": (c_size_t, [c_int, c_int]),
     "moe_group_wide": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
@@ -221,6 +254,190 @@ def moe_group_wide(keys, nkeys, counts, offsets, perm, scratch, stream=None):
     _check("moe_group_wide", load().moe_group_wide(_p(keys), n, nkeys, _p(counts), _p(offsets), _p(perm),
                                                    _p(scratch), _stream(stream)))
     return counts, offsets, perm
+
+
+# --------------------------------------------------------- around the experts
+#
+# These calls take a descriptor made once (make_router, make_norm, make_lora) and
+# tensors that are checked on every call: shape, type, density and one device,
+# which must be the current one.
+
+def _ptr(name, what, t, shape, dtypes, dev):
+    """The address of a dense GPU tensor of this shape and one of these types."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {what} is {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: {what} must be dense (row-major, contiguous)")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: {what} is on {t.device}, not on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _current(name, t):
+    """Device index of a call's first tensor, which must be the current device."""
+    import torch
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: tensors must be on the GPU")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name}: the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _types():
+    import torch
+    return {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _plan_tensor(name, what, t, shape, dtype):
+    """Checks a tensor that a descriptor keeps (on whatever device it is)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {what} is {t.dtype}, not {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: {what} must be dense (row-major, contiguous)")
+    return t.data_ptr()
+
+
+def _one_device(name, tensors):
+    devs = {t.get_device() for t in tensors if t is not None}
+    if len(devs) > 1:
+        raise ValueError(f"{name}: tensors on different devices")
+    return devs.pop() if devs else None
+
+
+def _same_device(name, desc, dev):
+    if desc._dev is not None and desc._dev != dev:
+        raise ValueError(f"{name}: the descriptor's tensors are on device {desc._dev}, the call's on cuda:{dev}")
+
+
+def make_router(E, k, scoring="sigmoid", groups=1, topk_groups=None, group_score="top2", renorm=True,
+                scale=1.0) -> moe_router:
+    """Settings of moe_route_groups; topk_groups None: every group stays."""
+    return moe_router(E, k, {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}[scoring], groups,
+                      groups if topk_groups is None else topk_groups,
+                      {"max": GROUP_MAX, "top2": GROUP_TOP2}[group_score], int(bool(renorm)), scale)
+
+
+def moe_route_groups(router: moe_router, logits, bias, ids, w, stream=None):
+    """logits [T, E] (float32 or bfloat16), bias [E] float32 or None -> ids [T, k] int32, w [T, k] float32."""
+    import torch
+    name, types = "moe_route_groups", _types()
+    dev = _current(name, logits)
+    T, E, k = logits.shape[0], router.E, router.k
+    st = load().moe_route_groups(
+        ctypes.byref(router), _ptr(name, "logits", logits, (T, E), types, dev), types[logits.dtype],
+        None if bias is None else _ptr(name, "bias", bias, (E,), (torch.float32,), dev), T,
+        _ptr(name, "ids", ids, (T, k), (torch.int32,), dev), _ptr(name, "w", w, (T, k), (torch.float32,), dev),
+        _stream(stream))
+    _check(name, st)
+    return ids, w
+
+
+def make_norm(H, eps=1e-6, pre=None, post=None, post_norm=None, weight_offset=0.0, gate="none", gate_act="none",
+              alpha=1.0) -> moe_norm:
+    """The norms around one block: pre [H] and post [H] are their weights (of
+    one type, or None: all ones); post_norm: whether the block's output is
+    normed (None: where post is given).  Keeps references to the weights."""
+    import torch
+    some = pre if pre is not None else post
+    wt = torch.float32 if some is None else some.dtype
+    if wt not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"make_norm: weights are {wt}")
+    pp = _plan_tensor("make_norm", "pre", pre, (H,), wt)
+    qp = _plan_tensor("make_norm", "post", post, (H,), wt)
+    n = moe_norm(H, eps, weight_offset, _types()[wt], pp, qp,
+                 int(post is not None if post_norm is None else bool(post_norm)),
+                 {"none": GATE_NONE, "channel": GATE_CHANNEL, "token": GATE_TOKEN, "full": GATE_FULL}[gate],
+                 {"none": GATE_LINEAR, "sigmoid": GATE_SIGMOID}[gate_act], alpha)
+    n._tensors = (pre, post)
+    n._dev = _one_device("make_norm", n._tensors)
+    return n
+
+
+def moe_norm_in(norm: moe_norm, x, out, stream=None):
+    """out [T, H] = RMS(x [T, H]; pre)."""
+    name, types = "moe_norm_in", _types()
+    dev = _current(name, x)
+    _same_device(name, norm, dev)
+    shape = (x.shape[0], norm.H)
+    st = load().moe_norm_in(ctypes.byref(norm), _ptr(name, "x", x, shape, types, dev), types[x.dtype], shape[0],
+                            _ptr(name, "out", out, shape, types, dev), types[out.dtype], _stream(stream))
+    _check(name, st)
+    return out
+
+
+def moe_norm_out(norm: moe_norm, y, residual, gate, out, next=None, next_out=None, stream=None):
+    """out [T, H] = residual + alpha * act(gate) * RMS(y; post) and, with next_out
+    [T, H], next_out = RMS(out before its rounding; next's pre).  gate: None, [H],
+    [T] or [T, H], as the norm says.  Without next_out, next is not used."""
+    name, types = "moe_norm_out", _types()
+    dev = _current(name, y)
+    _same_device(name, norm, dev)
+    T, H = y.shape[0], norm.H
+    shape = (T, H)
+    if residual.dtype != out.dtype:
+        raise TypeError(f"{name}: residual is {residual.dtype}, out is {out.dtype}")
+    gp = gt = np_ = nt = nd = None
+    if norm.gate != GATE_NONE and gate is None:
+        raise ValueError(f"{name}: the norm has a gate, the call has none")
+    if gate is not None:
+        if norm.gate == GATE_NONE:
+            raise ValueError(f"{name}: the norm has no gate")
+        gp = _ptr(name, "gate", gate, ((H,), (T,), shape)[norm.gate - 1], types, dev)
+        gt = types[gate.dtype]
+    if next_out is not None:
+        if next is None:
+            raise ValueError(f"{name}: next_out needs the next block's norm")
+        _same_device(name, next, dev)
+        np_, nt, nd = _ptr(name, "next_out", next_out, shape, types, dev), types[next_out.dtype], ctypes.byref(next)
+    st = load().moe_norm_out(
+        ctypes.byref(norm), _ptr(name, "y", y, shape, types, dev), types[y.dtype],
+        _ptr(name, "residual", residual, shape, types, dev), gp, gt or 0, T, _ptr(name, "out", out, shape, types, dev),
+        types[out.dtype], nd, np_, nt or 0, _stream(stream))
+    _check(name, st)
+    return out
+
+
+def make_lora(a, b, scale=None, ranks=None) -> moe_lora:
+    """A bank of adapters: a [num, r, K] and b [num, N, r] bfloat16, scale [num]
+    float32 or None, ranks [num] int32 or None (all r).  Keeps references."""
+    import torch
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("make_lora: a is [num, r, K] and b [num, N, r]")
+    num, r, K = a.shape
+    N = b.shape[1]
+    m = moe_lora(K, N, r, num, _plan_tensor("make_lora", "a", a, (num, r, K), torch.bfloat16),
+                 _plan_tensor("make_lora", "b", b, (num, N, r), torch.bfloat16),
+                 _plan_tensor("make_lora", "scale", scale, (num,), torch.float32),
+                 _plan_tensor("make_lora", "ranks", ranks, (num,), torch.int32))
+    m._tensors = (a, b, scale, ranks)
+    m._dev = _one_device("make_lora", m._tensors)
+    return m
+
+
+def moe_lora_add(lora: moe_lora, x, adapter_ids, base, out, stream=None):
+    """out [T, N] = base [T, N] (or zeros) + scale * B (A x [T, K]) with each token's
+    adapter, adapter_ids [T] int32 (outside the bank: none)."""
+    import torch
+    name, types = "moe_lora_add", _types()
+    dev = _current(name, x)
+    _same_device(name, lora, dev)
+    T = x.shape[0]
+    if base is not None and base.dtype != out.dtype:
+        raise TypeError(f"{name}: base is {base.dtype}, out is {out.dtype}")
+    st = load().moe_lora_add(
+        ctypes.byref(lora), _ptr(name, "x", x, (T, lora.K), types, dev), types[x.dtype], T,
+        _ptr(name, "adapter_ids", adapter_ids, (T,), (torch.int32,), dev),
+        None if base is None else _ptr(name, "base", base, (T, lora.N), types, dev),
+        _ptr(name, "out", out, (T, lora.N), types, dev), types[out.dtype], _stream(stream))
+    _check(name, st)
+    return out
 
 
 # ----------------------------------------------------------------- expert MLP
@@ -451,8 +668,8 @@ class Cache:
 # --------------------------------------------------------------------- timing
 
 PROF_KINDS = ("route", "router_logits", "gateup", "down", "combine", "group", "plan", "quant",
-              "gemm_gateup", "gemm_down", "dequant", "read", "cache", "fused", "scratch")
-MOE_PROF_KINDS = 16
+              "gemm_gateup", "gemm_down", "dequant", "read", "cache", "fused", "scratch", "norm", "lora")
+MOE_PROF_KINDS = 24
 
 
 def moe_profile_begin(max_launches: int):

@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <string>
@@ -69,6 +70,16 @@ moe_status launch_fused_b1s(const moe_layer* L, const float* logits, int E, cons
                             float* w, uint16_t* h, void* out, uint32_t* sync, hipStream_t s);
 moe_status launch_decode_mfma(const moe_layer* Lr, const void* x, int T, int k, const int32_t* slot_ids, const float* w,
                               void* out, uint16_t* h, float* y, int32_t* plan, hipStream_t s);
+
+moe_status launch_route_groups(const moe_router* R, const void* logits, moe_dtype lt, const float* bias, int T,
+                               int32_t* ids, float* w, hipStream_t s);
+moe_status launch_norm_in(const moe_norm* n, const void* x, moe_dtype xt, int T, void* out, moe_dtype ot,
+                          hipStream_t s);
+moe_status launch_norm_out(const moe_norm* n, const void* y, moe_dtype yt, const void* residual, const void* gate,
+                           moe_dtype gt, int T, void* out, moe_dtype rt, const moe_norm* next, void* next_out,
+                           moe_dtype nt, hipStream_t s);
+moe_status launch_lora(const moe_lora* L, const void* x, moe_dtype xt, int T, const int32_t* ids, const void* base,
+                       void* out, moe_dtype yt, hipStream_t s);
 
 static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -352,6 +363,126 @@ moe_status moe_debug_stream_read(const void* buf, size_t bytes, uint32_t* sink, 
           "moe_debug_stream_read: buf must be 16-byte aligned and bytes a multiple of 16");
   if (bytes == 0) return MOE_OK;
   return launch_stream_read(buf, bytes, sink, (hipStream_t)stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ around the experts
+
+namespace {
+
+constexpr int kMaxTokens = 1 << 20;  // rows of the calls below: a grid of 1024-thread workgroups stays below 2^32 threads
+
+bool is_dtype(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16; }
+size_t dsize(moe_dtype t) { return t == MOE_BF16 ? 2 : 4; }
+
+moe_status check_norm(const moe_norm* n, const char* who) {
+  REQUIRE(n, MOE_EINVAL, "%s: norm is NULL", who);
+  REQUIRE(n->H >= 1 && n->H <= 16384, MOE_ESHAPE, "%s: H=%d outside 1..16384", who, n->H);
+  REQUIRE(n->eps >= 0.0f && std::isfinite(n->eps), MOE_EINVAL, "%s: eps=%g must be finite and >= 0", who, (double)n->eps);
+  REQUIRE(std::isfinite(n->weight_offset) && std::isfinite(n->alpha), MOE_EINVAL,
+          "%s: weight_offset and alpha must be finite", who);
+  REQUIRE(is_dtype(n->wt), MOE_EINVAL, "%s: bad weight dtype %d", who, (int)n->wt);
+  REQUIRE(aligned(n->pre_w, dsize(n->wt)) && aligned(n->post_w, dsize(n->wt)), MOE_EINVAL,
+          "%s: norm weights must be aligned to their element", who);
+  REQUIRE(n->post_norm == 0 || n->post_norm == 1, MOE_EINVAL, "%s: post_norm=%d", who, n->post_norm);
+  REQUIRE(n->gate >= MOE_GATE_NONE && n->gate <= MOE_GATE_FULL, MOE_EINVAL, "%s: gate=%d", who, n->gate);
+  REQUIRE(n->gate_act == MOE_GATE_LINEAR || n->gate_act == MOE_GATE_SIGMOID, MOE_EINVAL, "%s: gate_act=%d", who,
+          n->gate_act);
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_route_groups(const moe_router* R, const void* logits, moe_dtype lt, const float* bias, int T,
+                            int32_t* ids, float* w, moe_stream_t stream) {
+  REQUIRE(R, MOE_EINVAL, "moe_route_groups: router is NULL");
+  REQUIRE(R->E >= 1 && R->E <= 1024, MOE_ESHAPE, "moe_route_groups: E=%d outside 1..1024", R->E);
+  REQUIRE(R->k >= 1 && R->k <= R->E && R->k <= 64, MOE_EINVAL,
+          "moe_route_groups: k=%d must satisfy 1 <= k <= min(E=%d, 64)", R->k, R->E);
+  REQUIRE(R->scoring == MOE_SCORE_SOFTMAX || R->scoring == MOE_SCORE_SIGMOID, MOE_EINVAL,
+          "moe_route_groups: scoring=%d", R->scoring);
+  REQUIRE(R->groups >= 1 && R->groups <= 64 && R->E % R->groups == 0, MOE_EINVAL,
+          "moe_route_groups: groups=%d must be 1..64 and divide E=%d", R->groups, R->E);
+  REQUIRE(R->topk_groups >= 1 && R->topk_groups <= R->groups, MOE_EINVAL,
+          "moe_route_groups: topk_groups=%d outside 1..groups=%d", R->topk_groups, R->groups);
+  REQUIRE(R->topk_groups * (R->E / R->groups) >= R->k, MOE_EINVAL,
+          "moe_route_groups: topk_groups=%d groups of %d experts hold fewer than k=%d", R->topk_groups,
+          R->E / R->groups, R->k);
+  REQUIRE(R->group_score == MOE_GROUP_MAX || R->group_score == MOE_GROUP_TOP2, MOE_EINVAL,
+          "moe_route_groups: group_score=%d", R->group_score);
+  REQUIRE(R->renorm == 0 || R->renorm == 1, MOE_EINVAL, "moe_route_groups: renorm=%d", R->renorm);
+  REQUIRE(std::isfinite(R->scale), MOE_EINVAL, "moe_route_groups: scale must be finite");
+  REQUIRE(is_dtype(lt), MOE_EINVAL, "moe_route_groups: bad dtype %d", (int)lt);
+  REQUIRE(T >= 0 && T <= kMaxTokens, MOE_ESHAPE, "moe_route_groups: T=%d outside 0..2^20", T);
+  if (T == 0) return MOE_OK;
+  REQUIRE(logits && ids && w, MOE_EINVAL, "moe_route_groups: NULL pointer");
+  REQUIRE(aligned(logits, dsize(lt)) && aligned(bias, 4) && aligned(ids, 4) && aligned(w, 4), MOE_EINVAL,
+          "moe_route_groups: pointers must be aligned to their element");
+  return launch_route_groups(R, logits, lt, bias, T, ids, w, (hipStream_t)stream);
+}
+
+moe_status moe_norm_in(const moe_norm* norm, const void* x, moe_dtype xt, int T, void* out, moe_dtype ot,
+                       moe_stream_t stream) {
+  const moe_status st = check_norm(norm, "moe_norm_in");
+  if (st != MOE_OK) return st;
+  REQUIRE(is_dtype(xt) && is_dtype(ot), MOE_EINVAL, "moe_norm_in: bad dtype %d or %d", (int)xt, (int)ot);
+  REQUIRE(T >= 0 && T <= kMaxTokens, MOE_ESHAPE, "moe_norm_in: T=%d outside 0..2^20", T);
+  if (T == 0) return MOE_OK;
+  REQUIRE(x && out, MOE_EINVAL, "moe_norm_in: NULL pointer");
+  REQUIRE(aligned(x, dsize(xt)) && aligned(out, dsize(ot)), MOE_EINVAL,
+          "moe_norm_in: pointers must be aligned to their element");
+  REQUIRE(x != out || xt == ot, MOE_EINVAL, "moe_norm_in: out may be x only where their types are equal");
+  return launch_norm_in(norm, x, xt, T, out, ot, (hipStream_t)stream);
+}
+
+moe_status moe_norm_out(const moe_norm* norm, const void* y, moe_dtype yt, const void* residual, const void* gate,
+                        moe_dtype gt, int T, void* out, moe_dtype rt, const moe_norm* next, void* next_out,
+                        moe_dtype nt, moe_stream_t stream) {
+  moe_status st = check_norm(norm, "moe_norm_out");
+  if (st != MOE_OK) return st;
+  if (next && (st = check_norm(next, "moe_norm_out (next)")) != MOE_OK) return st;
+  REQUIRE(!next == !next_out, MOE_EINVAL, "moe_norm_out: next and next_out must both be given or both be NULL");
+  REQUIRE(!next || next->H == norm->H, MOE_ESHAPE, "moe_norm_out: next norm has H=%d, not %d", next ? next->H : 0,
+          norm->H);
+  REQUIRE(is_dtype(yt) && is_dtype(rt) && (!next || is_dtype(nt)) && (norm->gate == MOE_GATE_NONE || is_dtype(gt)),
+          MOE_EINVAL, "moe_norm_out: bad dtype (y %d, residual %d, gate %d, next %d)", (int)yt, (int)rt, (int)gt,
+          (int)nt);
+  REQUIRE(T >= 0 && T <= kMaxTokens, MOE_ESHAPE, "moe_norm_out: T=%d outside 0..2^20", T);
+  if (T == 0) return MOE_OK;
+  REQUIRE(y && residual && out, MOE_EINVAL, "moe_norm_out: NULL pointer");
+  REQUIRE((norm->gate == MOE_GATE_NONE) == !gate, MOE_EINVAL, "moe_norm_out: gate=%d needs %s gate pointer",
+          norm->gate, norm->gate == MOE_GATE_NONE ? "no" : "a");
+  REQUIRE(aligned(y, dsize(yt)) && aligned(residual, dsize(rt)) && aligned(out, dsize(rt)) &&
+              (!gate || aligned(gate, dsize(gt))) && (!next || aligned(next_out, dsize(nt))),
+          MOE_EINVAL, "moe_norm_out: pointers must be aligned to their element");
+  REQUIRE(out != next_out, MOE_EINVAL, "moe_norm_out: out and next_out are the same buffer");
+  REQUIRE((out != y || yt == rt) && (!next || ((next_out != y || yt == nt) && (next_out != residual || rt == nt))),
+          MOE_EINVAL, "moe_norm_out: an output may be an input's buffer only where their types are equal");
+  REQUIRE(!gate || (gate != out && gate != next_out), MOE_EINVAL, "moe_norm_out: gate may not be an output's buffer");
+  return launch_norm_out(norm, y, yt, residual, gate, gt, T, out, rt, next, next_out, nt, (hipStream_t)stream);
+}
+
+moe_status moe_lora_add(const moe_lora* L, const void* x, moe_dtype xt, int T, const int32_t* adapter_ids,
+                        const void* base, void* out, moe_dtype yt, moe_stream_t stream) {
+  REQUIRE(L, MOE_EINVAL, "moe_lora_add: lora is NULL");
+  REQUIRE(L->K >= 1 && L->K <= 65536 && L->N >= 1 && L->N <= 65536, MOE_ESHAPE,
+          "moe_lora_add: K=%d N=%d outside 1..65536", L->K, L->N);
+  REQUIRE(L->r >= 1 && L->r <= 128, MOE_ESHAPE, "moe_lora_add: r=%d outside 1..128", L->r);
+  REQUIRE(L->num >= 0 && L->num <= 65536, MOE_ESHAPE, "moe_lora_add: num=%d outside 0..65536", L->num);
+  REQUIRE(L->num == 0 || (L->a && L->b), MOE_EINVAL, "moe_lora_add: the bank is NULL with num=%d", L->num);
+  REQUIRE(aligned(L->a, 2) && aligned(L->b, 2) && aligned(L->scale, 4) && aligned(L->ranks, 4), MOE_EINVAL,
+          "moe_lora_add: the bank must be aligned to its elements");
+  REQUIRE(is_dtype(xt) && is_dtype(yt), MOE_EINVAL, "moe_lora_add: bad dtype %d or %d", (int)xt, (int)yt);
+  REQUIRE(T >= 0 && T <= kMaxTokens, MOE_ESHAPE, "moe_lora_add: T=%d outside 0..2^20", T);
+  if (T == 0) return MOE_OK;
+  REQUIRE(x && adapter_ids && out, MOE_EINVAL, "moe_lora_add: NULL pointer");
+  REQUIRE(aligned(x, dsize(xt)) && aligned(adapter_ids, 4) && aligned(base, dsize(yt)) && aligned(out, dsize(yt)),
+          MOE_EINVAL, "moe_lora_add: pointers must be aligned to their element");
+  REQUIRE(x != out, MOE_EINVAL, "moe_lora_add: out may not be x");
+  return launch_lora(L, x, xt, T, adapter_ids, base, out, yt, (hipStream_t)stream);
 }
 
 }  // extern "C"
