@@ -1,0 +1,115 @@
+// Chunks of eight consecutive bf16 or fp32 elements at any element-aligned
+// address: one or two 16-byte accesses where all eight are there (the hardware
+// takes global accesses at any alignment), single elements at the end of a row.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+struct __attribute__((packed, aligned(2))) Packed8h {
+  uint32_t x, y, z, w;
+};
+struct __attribute__((packed, aligned(4))) Packed4f {
+  float x, y, z, w;
+};
+
+__device__ __forceinline__ uint4 ld8h(const uint16_t* p) {
+  const Packed8h v = *(const Packed8h*)p;
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+
+__device__ __forceinline__ void st8h(uint16_t* p, uint4 v) { *(Packed8h*)p = Packed8h{v.x, v.y, v.z, v.w}; }
+
+// the first n of eight bf16 elements, the others zero
+__device__ __forceinline__ uint32_t ld2h_part(const uint16_t* p, int n) {
+  const uint32_t lo = n > 0 ? p[0] : 0, hi = n > 1 ? p[1] : 0;
+  return lo | (hi << 16);
+}
+
+__device__ __forceinline__ uint4 ld8h_part(const uint16_t* p, int n) {
+  return make_uint4(ld2h_part(p, n), ld2h_part(p + 2, n - 2), ld2h_part(p + 4, n - 4), ld2h_part(p + 6, n - 6));
+}
+
+__device__ __forceinline__ uint4 ld8h_to(const uint16_t* p, int n) { return n >= 8 ? ld8h(p) : ld8h_part(p, n); }
+
+__device__ __forceinline__ f32x8 ld8f(const float* p) {
+  const Packed4f a = *(const Packed4f*)p, b = *(const Packed4f*)(p + 4);
+  return f32x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
+__device__ __forceinline__ float ld1f_if(const float* p, bool there) { return there ? *p : 0.0f; }
+
+__device__ __forceinline__ f32x8 ld8f_to(const float* p, int n) {
+  if (n >= 8) return ld8f(p);
+  return f32x8{ld1f_if(p, n > 0),     ld1f_if(p + 1, n > 1), ld1f_if(p + 2, n > 2), ld1f_if(p + 3, n > 3),
+               ld1f_if(p + 4, n > 4), ld1f_if(p + 5, n > 5), ld1f_if(p + 6, n > 6), 0.0f};
+}
+
+__device__ __forceinline__ f32x8 widen(uint4 h) {
+  return f32x8{bf16_lo(h.x), bf16_hi(h.x), bf16_lo(h.y), bf16_hi(h.y),
+               bf16_lo(h.z), bf16_hi(h.z), bf16_lo(h.w), bf16_hi(h.w)};
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return (uint32_t)f32_to_bf16(lo) | ((uint32_t)f32_to_bf16(hi) << 16);
+}
+
+template <bool BF16>
+__device__ __forceinline__ f32x8 load8(const void* p, size_t at, int n) {
+  if constexpr (BF16)
+    return widen(ld8h_to((const uint16_t*)p + at, n));
+  else
+    return ld8f_to((const float*)p + at, n);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void* p, size_t at, int n, f32x8 v) {
+  if (BF16) {
+    uint16_t* o = (uint16_t*)p + at;
+    if (n >= 8) {
+      st8h(o, make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) o[e] = f32_to_bf16(v[e]);
+    }
+  } else {
+    float* o = (float*)p + at;
+    if (n >= 8) {
+      *(Packed4f*)o = Packed4f{v[0], v[1], v[2], v[3]};
+      *(Packed4f*)(o + 4) = Packed4f{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) o[e] = v[e];
+    }
+  }
+}
+
+// A chunk whose type is known at run time only (the same for the whole launch):
+// as it was loaded, and widened.
+__device__ __forceinline__ f32x8 load8_raw(const void* p, bool bf16, size_t at, int n) {
+  if (!bf16) return ld8f_to((const float*)p + at, n);
+  const uint4 h = ld8h_to((const uint16_t*)p + at, n);
+  return f32x8{__uint_as_float(h.x), __uint_as_float(h.y), __uint_as_float(h.z), __uint_as_float(h.w), 0, 0, 0, 0};
+}
+
+__device__ __forceinline__ f32x8 widen_raw(f32x8 v, bool bf16) {
+  if (!bf16) return v;
+  return widen(make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+}
+
+__device__ __forceinline__ float load1(const void* p, bool bf16, size_t at) {
+  return bf16 ? bf(((const uint16_t*)p)[at]) : ((const float*)p)[at];
+}
+
+// 1 / (1 + e^-g): the hardware's exponential of 2 and reciprocal, each within a
+// step of fp32, the argument's rounding growing with |g|
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+}  // namespace moe

@@ -11,7 +11,7 @@
 // Both compute A x whole in every workgroup that needs it (from the caches
 // after the first) and split the outputs over workgroups, so the call is one
 // launch and needs no workspace.
-#include "common.h"
+#include "chunk_dev.h"
 
 namespace moe {
 
@@ -21,62 +21,6 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kMaxRank = 128;
-
-__device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-
-// eight elements at an address aligned to one element only
-struct __attribute__((packed, aligned(2))) Packed8h {
-  uint32_t x, y, z, w;
-};
-struct __attribute__((packed, aligned(4))) Packed4f {
-  float x, y, z, w;
-};
-
-__device__ __forceinline__ uint4 ld8h(const uint16_t* p) {
-  const Packed8h v = *(const Packed8h*)p;
-  return make_uint4(v.x, v.y, v.z, v.w);
-}
-
-__device__ __forceinline__ void st8h(uint16_t* p, uint4 v) { *(Packed8h*)p = Packed8h{v.x, v.y, v.z, v.w}; }
-
-// the first n of eight bf16 elements, the others zero
-__device__ __forceinline__ uint32_t ld2h_part(const uint16_t* p, int n) {
-  const uint32_t lo = n > 0 ? p[0] : 0, hi = n > 1 ? p[1] : 0;
-  return lo | (hi << 16);
-}
-
-__device__ __forceinline__ uint4 ld8h_part(const uint16_t* p, int n) {
-  return make_uint4(ld2h_part(p, n), ld2h_part(p + 2, n - 2), ld2h_part(p + 4, n - 4), ld2h_part(p + 6, n - 6));
-}
-
-__device__ __forceinline__ uint4 ld8h_to(const uint16_t* p, int n) { return n >= 8 ? ld8h(p) : ld8h_part(p, n); }
-
-__device__ __forceinline__ void ld8f(const float* p, float (&v)[8]) {
-  const Packed4f a = *(const Packed4f*)p, b = *(const Packed4f*)(p + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-
-__device__ __forceinline__ void ld8f_to(const float* p, int n, float (&v)[8]) {
-  if (n >= 8) {
-    ld8f(p, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v[e] = 0.0f;
-      if (e < n) v[e] = p[e];
-    }
-  }
-}
-
-__device__ __forceinline__ void widen(uint4 h, float (&v)[8]) {
-  const uint32_t u[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[2 * e] = bf16_lo(u[e]), v[2 * e + 1] = bf16_hi(u[e]);
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  return (uint32_t)f32_to_bf16(lo) | ((uint32_t)f32_to_bf16(hi) << 16);
-}
 
 __device__ __forceinline__ int rank_of(const moe_lora& L, int id) {
   return L.ranks ? max(0, min(L.ranks[id], L.r)) : L.r;
@@ -111,28 +55,20 @@ __global__ __launch_bounds__(kTokThreads) void token_kernel(moe_lora L, const vo
     const size_t at = (size_t)t * K;
 #pragma unroll 4
     for (int k = lane * 8; k < kfull; k += 512) {
-      float xv[8], av[8];
-      if (XBF16)
-        widen(ld8h((const uint16_t*)x + at + k), xv);
-      else
-        ld8f((const float*)x + at + k, xv);
+      const f32x8 xv = load8<XBF16>(x, at + k, 8);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        widen(ld8h(row[i] + k), av);
+        const f32x8 av = widen(ld8h(row[i] + k));
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[i] = fmaf(xv[e], av[e], acc[i]);
       }
     }
     const int k = kfull + lane * 8;
     if (k < K) {
-      float xv[8], av[8];
-      if (XBF16)
-        widen(ld8h_to((const uint16_t*)x + at + k, K - k), xv);
-      else
-        ld8f_to((const float*)x + at + k, K - k, xv);
+      const f32x8 xv = load8<XBF16>(x, at + k, K - k);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        widen(ld8h_to(row[i] + k, K - k), av);
+        const f32x8 av = widen(ld8h_to(row[i] + k, K - k));
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[i] = fmaf(xv[e], av[e], acc[i]);
       }
@@ -148,8 +84,7 @@ __global__ __launch_bounds__(kTokThreads) void token_kernel(moe_lora L, const vo
     const size_t at = (size_t)t * L.N + n;
     float acc = 0.f;
     for (int j = 0; j < rank; j += 8) {
-      float bv[8];
-      widen(ld8h_to(B + (size_t)n * L.r + j, rank - j), bv);
+      const f32x8 bv = widen(ld8h_to(B + (size_t)n * L.r + j, rank - j));
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc = fmaf(v[j + e], bv[e], acc);
     }
@@ -199,55 +134,29 @@ __device__ __forceinline__ uint16_t take_bf16(float& f) {
 template <bool YBF16>
 struct Out {
   uint4 h[2];
-  float f[YBF16 ? 1 : 16];
+  f32x8 f[2];
 
   __device__ __forceinline__ void load(const void* base, size_t at, int n) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (YBF16) {
+      if constexpr (YBF16)
         h[i] = base ? ld8h_to((const uint16_t*)base + at + 8 * i, n - 8 * i) : make_uint4(0, 0, 0, 0);
-      } else {
-        float b[8] = {};
-        if (base) ld8f_to((const float*)base + at + 8 * i, n - 8 * i, b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[YBF16 ? 0 : 8 * i + e] = b[e];
-      }
+      else
+        f[i] = base ? ld8f_to((const float*)base + at + 8 * i, n - 8 * i) : f32x8(0.f);
     }
   }
 
   __device__ __forceinline__ void store(void* out, size_t at, int n, const v4f (&d)[4]) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float w[8];
-      if (YBF16) {
-        widen(h[i], w);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = f[YBF16 ? 0 : 8 * i + e];
-      }
+      f32x8 w;
+      if constexpr (YBF16)
+        w = widen(h[i]);
+      else
+        w = f[i];
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] += d[2 * i + (e >> 2)][e & 3];
-      const int left = n - 8 * i;
-      if (YBF16) {
-        uint16_t* po = (uint16_t*)out + at + 8 * i;
-        if (left >= 8) {
-          st8h(po, make_uint4(pack2(w[0], w[1]), pack2(w[2], w[3]), pack2(w[4], w[5]), pack2(w[6], w[7])));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < left) po[e] = f32_to_bf16(w[e]);
-        }
-      } else {
-        float* po = (float*)out + at + 8 * i;
-        if (left >= 8) {
-          *(Packed4f*)po = Packed4f{w[0], w[1], w[2], w[3]};
-          *(Packed4f*)(po + 4) = Packed4f{w[4], w[5], w[6], w[7]};
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < left) po[e] = w[e];
-        }
-      }
+      store8<YBF16>(out, at + 8 * i, n - 8 * i, w);
     }
   }
 };
@@ -301,14 +210,11 @@ __device__ __forceinline__ void shrink_block(const void* __restrict__ xrow, cons
     const float* xp = (const float*)xrow + k;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float xv[8], av[NP][8];
-      if (FULL)
-        ld8f(xp + 8 * h, xv);
-      else
-        ld8f_to(xp + 8 * h, K - k - 8 * h, xv);
+      const f32x8 xv = FULL ? ld8f(xp + 8 * h) : ld8f_to(xp + 8 * h, K - k - 8 * h);
+      f32x8 av[NP];
 #pragma unroll
       for (int p = 0; p < NP; ++p)
-        widen(FULL ? ld8h(arow[p] + k + 8 * h) : ld8h_to(arow[p] + k + 8 * h, K - k - 8 * h), av[p]);
+        av[p] = widen(FULL ? ld8h(arow[p] + k + 8 * h) : ld8h_to(arow[p] + k + 8 * h, K - k - 8 * h));
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll

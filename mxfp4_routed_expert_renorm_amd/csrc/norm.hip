@@ -4,84 +4,171 @@
 //
 //   r = residual + alpha * act(gate) * RMS(y; w_post),  next = RMS(r; w_pre)
 //
-// One workgroup owns one row, which it keeps in LDS as fp32 between the two
-// sums, so every input is read once and out may overwrite an input.
-#include "common.h"
+// A row belongs to a group of 64 to 1024 threads of one workgroup and stays in
+// their registers from its only read to its writes, so out may overwrite an
+// input.  A thread holds V chunks of eight consecutive elements; everything a
+// row needs (weights and gate too) is requested before the first sum is formed.
+#include "chunk_dev.h"
 
 namespace moe {
 
 namespace {
 
-__device__ __forceinline__ float ld(const void* p, bool bf16, size_t i) {
-  return bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16) : ((const float*)p)[i];
-}
-
-__device__ __forceinline__ void st(void* p, bool bf16, size_t i, float v) {
-  if (bf16)
-    ((uint16_t*)p)[i] = f32_to_bf16(v);
-  else
-    ((float*)p)[i] = v;
-}
-
 struct NormArgs {
   const void *y, *residual, *gate, *post_w, *pre_w;
   void *out, *next_out;
-  float eps, offset, alpha, next_eps, next_offset;
-  int H, gate_kind;
-  bool post, sigmoid, ybf, rbf, gbf, wbf, nwbf, nbf;
+  float eps, offset, alpha, next_eps, next_offset, inv_h;
+  int T, H, gate_kind, per_row;  // per_row: threads a row, a power of two >= 64
+  bool post, sigmoid, gbf, wbf, nwbf;
 };
 
-__device__ __forceinline__ float block_sum(float v, float* red) {
+// The sum over a row's threads, in all of them.  red: one float a wavefront.
+__device__ __forceinline__ float row_sum(float v, int per_row, float* red) {
   v = wave_sum(v);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  if (per_row == 64) return v;
+  const int wave = threadIdx.x >> 6, waves = per_row >> 6, first = wave & ~(waves - 1);
+  if ((threadIdx.x & 63) == 0) red[wave] = v;
   __syncthreads();
-  v = red[0] + red[1] + red[2] + red[3];
-  __syncthreads();
+  v = 0.f;
+  for (int i = 0; i < waves; ++i) v += red[first + i];
   return v;
 }
 
-__global__ __launch_bounds__(256) void norm_kernel(NormArgs a) {
-  extern __shared__ float row[];
-  __shared__ float red[4];
-  const size_t at = (size_t)blockIdx.x * a.H;
+template <bool XBF16, bool OBF16, int V>
+__global__ __launch_bounds__(1024) void norm_in_kernel(NormArgs a) {
+  __shared__ float red[16];
+  const int in_row = threadIdx.x & (a.per_row - 1);
+  const int row = blockIdx.x * (blockDim.x / a.per_row) + threadIdx.x / a.per_row;
+  const bool live = row < a.T;
+  const size_t at = (size_t)min(row, a.T - 1) * a.H;
+  f32x8 x[V], w[V];
   float ss = 0.f;
-  for (int i = threadIdx.x; i < a.H; i += 256) {
-    const float v = ld(a.y, a.ybf, at + i);
-    row[i] = v;
-    ss = fmaf(v, v, ss);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = (i * a.per_row + in_row) * 8;
+    x[i] = load8<XBF16>(a.y, at + e, a.H - e);
+    w[i] = a.pre_w ? load8_raw(a.pre_w, a.nwbf, e, a.H - e) : f32x8(0.f);
   }
-  if (a.out) {
-    const float rs = a.post ? 1.0f / sqrtf(block_sum(ss, red) / (float)a.H + a.eps) : 1.0f;
-    ss = 0.f;
-    for (int i = threadIdx.x; i < a.H; i += 256) {
-      float z = row[i] * rs;
-      if (a.post && a.post_w) z *= a.offset + ld(a.post_w, a.wbf, i);
-      if (a.gate_kind != MOE_GATE_NONE) {
-        float g = ld(a.gate, a.gbf,
-                     a.gate_kind == MOE_GATE_CHANNEL ? (size_t)i
-                     : a.gate_kind == MOE_GATE_TOKEN ? (size_t)blockIdx.x
-                                                     : at + i);
-        if (a.sigmoid) g = 1.0f / (1.0f + expf(-g));
-        z *= g;
-      }
-      const float r = fmaf(a.alpha, z, ld(a.residual, a.rbf, at + i));
-      row[i] = r;
-      ss = fmaf(r, r, ss);
-    }
-    for (int i = threadIdx.x; i < a.H; i += 256) st(a.out, a.rbf, at + i, row[i]);
-  }
-  if (!a.next_out) return;
-  const float rs = 1.0f / sqrtf(block_sum(ss, red) / (float)a.H + a.next_eps);
-  for (int i = threadIdx.x; i < a.H; i += 256) {
-    const float w = a.pre_w ? a.next_offset + ld(a.pre_w, a.nwbf, i) : 1.0f;
-    st(a.next_out, a.nbf, at + i, row[i] * rs * w);
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(x[i][j], x[i][j], ss);
+  const float rs = rsqrtf(fmaf(row_sum(ss, a.per_row, red), a.inv_h, a.next_eps));
+  if (!live) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = (i * a.per_row + in_row) * 8;
+    f32x8 o = x[i] * rs;
+    if (a.pre_w) o *= a.next_offset + widen_raw(w[i], a.nwbf);
+    store8<OBF16>(a.next_out, at + e, a.H - e, o);
   }
 }
 
-moe_status run(const NormArgs& a, int T, hipStream_t s) {
-  launch(MOE_PROF_NORM, norm_kernel, dim3(T), dim3(256), (size_t)a.H * 4, s, a);
-  MOE_LAUNCH_CHECK();
-  return MOE_OK;
+template <bool YBF16, bool RBF16, bool NBF16, int V>
+__global__ __launch_bounds__(1024) void norm_out_kernel(NormArgs a) {
+  __shared__ float red[2][16];
+  const int in_row = threadIdx.x & (a.per_row - 1);
+  const int row = blockIdx.x * (blockDim.x / a.per_row) + threadIdx.x / a.per_row;
+  const bool live = row < a.T;
+  const size_t at = (size_t)min(row, a.T - 1) * a.H;
+  f32x8 y[V], r[V], w[V], g[V], nw[V];
+  const bool elementwise = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL;
+  float tok = 1.f;
+  if (a.gate_kind == MOE_GATE_TOKEN) tok = load1(a.gate, a.gbf, min(row, a.T - 1));
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = (i * a.per_row + in_row) * 8, n = a.H - e;
+    y[i] = load8<YBF16>(a.y, at + e, n);
+    r[i] = load8<RBF16>(a.residual, at + e, n);
+    g[i] = elementwise ? load8_raw(a.gate, a.gbf, a.gate_kind == MOE_GATE_FULL ? at + e : e, n) : f32x8(0.f);
+    w[i] = a.post && a.post_w ? load8_raw(a.post_w, a.wbf, e, n) : f32x8(0.f);
+    nw[i] = a.next_out && a.pre_w ? load8_raw(a.pre_w, a.nwbf, e, n) : f32x8(0.f);
+  }
+  float c = a.alpha;
+  if (a.post) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(y[i][j], y[i][j], ss);
+    const float rs = rsqrtf(fmaf(row_sum(ss, a.per_row, red[0]), a.inv_h, a.eps));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      y[i] *= rs;
+      if (a.post_w) y[i] *= a.offset + widen_raw(w[i], a.wbf);
+    }
+  }
+  if (a.gate_kind == MOE_GATE_TOKEN) c *= a.sigmoid ? sigmoid(tok) : tok;
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (elementwise) {
+      f32x8 f = widen_raw(g[i], a.gbf);
+      if (a.sigmoid) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = sigmoid(f[j]);
+      }
+      y[i] *= f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      r[i][j] = fmaf(c, y[i][j], r[i][j]);
+      ss = fmaf(r[i][j], r[i][j], ss);
+    }
+  }
+  if (live) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = (i * a.per_row + in_row) * 8;
+      store8<RBF16>(a.out, at + e, a.H - e, r[i]);
+    }
+  }
+  if (!a.next_out) return;
+  const float rs = rsqrtf(fmaf(row_sum(ss, a.per_row, red[1]), a.inv_h, a.next_eps));
+  if (!live) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = (i * a.per_row + in_row) * 8;
+    r[i] *= rs;
+    if (a.pre_w) r[i] *= a.next_offset + widen_raw(nw[i], a.nwbf);
+    store8<NBF16>(a.next_out, at + e, a.H - e, r[i]);
+  }
+}
+
+struct Shape {
+  dim3 grid, block;
+  int v;
+};
+
+// Two chunks a thread where there are rows enough to fill the card, one where a
+// row's latency is what counts.
+Shape shape(NormArgs& a) {
+  const int chunks = (a.H + 7) / 8;
+  const int v = chunks > 1024 || a.T > 256 ? 2 : 1;
+  int per = 64;
+  while (per * v < chunks) per *= 2;
+  const int block = max(per, 256), rows = block / per;
+  a.per_row = per;
+  a.inv_h = 1.0f / (float)a.H;
+  return {dim3((a.T + rows - 1) / rows), dim3(block), v};
+}
+
+template <bool XB, bool OB>
+void run_in(NormArgs& a, hipStream_t s) {
+  const Shape h = shape(a);
+  if (h.v == 1)
+    launch(MOE_PROF_NORM, norm_in_kernel<XB, OB, 1>, h.grid, h.block, 0, s, a);
+  else
+    launch(MOE_PROF_NORM, norm_in_kernel<XB, OB, 2>, h.grid, h.block, 0, s, a);
+}
+
+template <bool YB, bool RB, bool NB>
+void run_out(NormArgs& a, hipStream_t s) {
+  const Shape h = shape(a);
+  if (h.v == 1)
+    launch(MOE_PROF_NORM, norm_out_kernel<YB, RB, NB, 1>, h.grid, h.block, 0, s, a);
+  else
+    launch(MOE_PROF_NORM, norm_out_kernel<YB, RB, NB, 2>, h.grid, h.block, 0, s, a);
 }
 
 }  // namespace
@@ -90,15 +177,20 @@ moe_status launch_norm_in(const moe_norm* n, const void* x, moe_dtype xt, int T,
                           hipStream_t s) {
   NormArgs a{};
   a.y = x;
-  a.ybf = xt == MOE_BF16;
+  a.T = T;
   a.H = n->H;
   a.pre_w = n->pre_w;
   a.nwbf = n->wt == MOE_BF16;
   a.next_eps = n->eps;
   a.next_offset = n->weight_offset;
   a.next_out = out;
-  a.nbf = ot == MOE_BF16;
-  return run(a, T, s);
+  const bool xb = xt == MOE_BF16, ob = ot == MOE_BF16;
+  if (xb)
+    ob ? run_in<true, true>(a, s) : run_in<true, false>(a, s);
+  else
+    ob ? run_in<false, true>(a, s) : run_in<false, false>(a, s);
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
 }
 
 moe_status launch_norm_out(const moe_norm* n, const void* y, moe_dtype yt, const void* residual, const void* gate,
@@ -106,10 +198,9 @@ moe_status launch_norm_out(const moe_norm* n, const void* y, moe_dtype yt, const
                            moe_dtype nt, hipStream_t s) {
   NormArgs a{};
   a.y = y;
-  a.ybf = yt == MOE_BF16;
   a.residual = residual;
   a.out = out;
-  a.rbf = rt == MOE_BF16;
+  a.T = T;
   a.H = n->H;
   a.eps = n->eps;
   a.offset = n->weight_offset;
@@ -127,9 +218,21 @@ moe_status launch_norm_out(const moe_norm* n, const void* y, moe_dtype yt, const
     a.next_eps = next->eps;
     a.next_offset = next->weight_offset;
     a.next_out = next_out;
-    a.nbf = nt == MOE_BF16;
   }
-  return run(a, T, s);
+  const bool yb = yt == MOE_BF16, rb = rt == MOE_BF16, nb = next && nt == MOE_BF16;
+  if (yb) {
+    if (rb)
+      nb ? run_out<true, true, true>(a, s) : run_out<true, true, false>(a, s);
+    else
+      nb ? run_out<true, false, true>(a, s) : run_out<true, false, false>(a, s);
+  } else {
+    if (rb)
+      nb ? run_out<false, true, true>(a, s) : run_out<false, true, false>(a, s);
+    else
+      nb ? run_out<false, false, true>(a, s) : run_out<false, false, false>(a, s);
+  }
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
 }
 
 }  // namespace moe
