@@ -277,18 +277,44 @@ def _ptr(name, what, t, shape, dtypes, dev):
 
 def _current(name, t):
     """Device index of a call's first tensor, which must be the current device."""
-    import torch
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name}: tensors must be on the GPU")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name}: the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    now = _torch().cuda.current_device()
+    if dev != now:
+        raise ValueError(f"{name}: the tensors are on cuda:{dev}, the current device is cuda:{now}")
     return dev
 
 
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_type_codes = None
+
+
 def _types():
-    import torch
-    return {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+    """Element types of activations and their codes."""
+    global _type_codes
+    if _type_codes is None:
+        torch = _torch()
+        _type_codes = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+    return _type_codes
+
+
+def _stream_of(stream, dev):
+    """The given stream, or the current one of the device (the raw handle: making
+    a stream object costs as much as a launch)."""
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
 def _plan_tensor(name, what, t, shape, dtype):
@@ -326,15 +352,14 @@ def make_router(E, k, scoring="sigmoid", groups=1, topk_groups=None, group_score
 
 def moe_route_groups(router: moe_router, logits, bias, ids, w, stream=None):
     """logits [T, E] (float32 or bfloat16), bias [E] float32 or None -> ids [T, k] int32, w [T, k] float32."""
-    import torch
-    name, types = "moe_route_groups", _types()
+    torch, name, types = _torch(), "moe_route_groups", _types()
     dev = _current(name, logits)
     T, E, k = logits.shape[0], router.E, router.k
     st = load().moe_route_groups(
         ctypes.byref(router), _ptr(name, "logits", logits, (T, E), types, dev), types[logits.dtype],
         None if bias is None else _ptr(name, "bias", bias, (E,), (torch.float32,), dev), T,
         _ptr(name, "ids", ids, (T, k), (torch.int32,), dev), _ptr(name, "w", w, (T, k), (torch.float32,), dev),
-        _stream(stream))
+        _stream_of(stream, dev))
     _check(name, st)
     return ids, w
 
@@ -367,7 +392,7 @@ def moe_norm_in(norm: moe_norm, x, out, stream=None):
     _same_device(name, norm, dev)
     shape = (x.shape[0], norm.H)
     st = load().moe_norm_in(ctypes.byref(norm), _ptr(name, "x", x, shape, types, dev), types[x.dtype], shape[0],
-                            _ptr(name, "out", out, shape, types, dev), types[out.dtype], _stream(stream))
+                            _ptr(name, "out", out, shape, types, dev), types[out.dtype], _stream_of(stream, dev))
     _check(name, st)
     return out
 
@@ -399,7 +424,7 @@ def moe_norm_out(norm: moe_norm, y, residual, gate, out, next=None, next_out=Non
     st = load().moe_norm_out(
         ctypes.byref(norm), _ptr(name, "y", y, shape, types, dev), types[y.dtype],
         _ptr(name, "residual", residual, shape, types, dev), gp, gt or 0, T, _ptr(name, "out", out, shape, types, dev),
-        types[out.dtype], nd, np_, nt or 0, _stream(stream))
+        types[out.dtype], nd, np_, nt or 0, _stream_of(stream, dev))
     _check(name, st)
     return out
 
@@ -424,8 +449,7 @@ def make_lora(a, b, scale=None, ranks=None) -> moe_lora:
 def moe_lora_add(lora: moe_lora, x, adapter_ids, base, out, stream=None):
     """out [T, N] = base [T, N] (or zeros) + scale * B (A x [T, K]) with each token's
     adapter, adapter_ids [T] int32 (outside the bank: none)."""
-    import torch
-    name, types = "moe_lora_add", _types()
+    torch, name, types = _torch(), "moe_lora_add", _types()
     dev = _current(name, x)
     _same_device(name, lora, dev)
     T = x.shape[0]
@@ -435,7 +459,7 @@ def moe_lora_add(lora: moe_lora, x, adapter_ids, base, out, stream=None):
         ctypes.byref(lora), _ptr(name, "x", x, (T, lora.K), types, dev), types[x.dtype], T,
         _ptr(name, "adapter_ids", adapter_ids, (T,), (torch.int32,), dev),
         None if base is None else _ptr(name, "base", base, (T, lora.N), types, dev),
-        _ptr(name, "out", out, (T, lora.N), types, dev), types[out.dtype], _stream(stream))
+        _ptr(name, "out", out, (T, lora.N), types, dev), types[out.dtype], _stream_of(stream, dev))
     _check(name, st)
     return out
 

@@ -14,6 +14,9 @@ __device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32
 struct __attribute__((packed, aligned(2))) Packed8h {
   uint32_t x, y, z, w;
 };
+struct __attribute__((packed, aligned(2))) Packed4h {
+  uint32_t x, y;
+};
 struct __attribute__((packed, aligned(4))) Packed4f {
   float x, y, z, w;
 };

@@ -13,6 +13,12 @@
 // launch and needs no workspace.
 #include "chunk_dev.h"
 
+#ifndef KG
+#define KG 256
+#endif
+#ifndef KT
+#define KT 128
+#endif
 namespace moe {
 
 namespace {
@@ -27,14 +33,106 @@ __device__ __forceinline__ int rank_of(const moe_lora& L, int id) {
 }
 
 // ------------------------------------------------------------ a token a workgroup
+//
+// A x: a wavefront takes R rows of A at a time, a lane eight K positions of each
+// at a stride of 512; R and the steps in flight keep 20 16-byte loads of a
+// wavefront outstanding.  B v: 1 to 16 lanes share a row of B, each with its
+// eight ranks of v in registers, so that a wavefront's loads are contiguous.
 
 constexpr int kTokThreads = 512, kTokWaves = kTokThreads / 64;
+constexpr int kTokOut = 1024;  // outputs gathered in LDS before they are written
+
+// eight products of a chunk of x with a chunk of a row of A, onto acc
+template <bool XBF16>
+struct XChunk;
+
+template <>
+struct XChunk<true> {
+  uint4 h;
+  __device__ __forceinline__ void load(const void* x, size_t at, int n) { h = ld8h_to((const uint16_t*)x + at, n); }
+  __device__ __forceinline__ float dot(uint4 a, float acc) const {
+    return dot2_bf16(h.w, a.w, dot2_bf16(h.z, a.z, dot2_bf16(h.y, a.y, dot2_bf16(h.x, a.x, acc))));
+  }
+};
+
+template <>
+struct XChunk<false> {
+  f32x8 f;
+  __device__ __forceinline__ void load(const void* x, size_t at, int n) { f = ld8f_to((const float*)x + at, n); }
+  __device__ __forceinline__ float dot(uint4 a, float acc) const {
+    const f32x8 w = widen(a);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc = fmaf(f[e], w[e], acc);
+    return acc;
+  }
+};
+
+// R rows of A from row j on with x's row at `at`: their sums, in every lane
+template <bool XBF16, int R, int S>
+__device__ __forceinline__ void token_rows(const void* __restrict__ x, size_t at, const uint16_t* __restrict__ A, int j,
+                                           int rank, int K, float (&acc)[R]) {
+  const int lane = threadIdx.x & 63;
+  const uint16_t* row[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) acc[i] = 0.f, row[i] = A + (size_t)min(j + i, rank - 1) * K;
+  int k = lane * 8;
+  for (; k - lane * 8 + 512 * S <= K; k += 512 * S) {
+    XChunk<XBF16> xv[S];
+    uint4 av[S][R];
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+      xv[u].load(x, at + k + 512 * u, 8);
+#pragma unroll
+      for (int i = 0; i < R; ++i) av[u][i] = ld8h(row[i] + k + 512 * u);
+    }
+#pragma unroll
+    for (int u = 0; u < S; ++u)
+#pragma unroll
+      for (int i = 0; i < R; ++i) acc[i] = xv[u].dot(av[u][i], acc[i]);
+  }
+  for (; k < K; k += 512) {
+    XChunk<XBF16> xv;
+    xv.load(x, at + k, K - k);
+#pragma unroll
+    for (int i = 0; i < R; ++i) acc[i] = xv.dot(ld8h_to(row[i] + k, K - k), acc[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) acc[i] = wave_sum(acc[i]);
+}
+
+// B v for the outputs n0 + wave .. of this workgroup's m into o, LANES lanes a row
+template <int LANES>
+__device__ __forceinline__ void token_outputs(const uint16_t* __restrict__ B, const float* v, int n0, int m, int r,
+                                              int rank, float* o) {
+  constexpr int kRows = 64 / LANES, kStep = kTokWaves * kRows, U = 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = (lane % LANES) * 8;
+  const int left = rank - j;  // <= 0: this lane has no ranks
+  f32x8 mine;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) mine[e] = v[min(j + e, kMaxRank - 1)];
+  for (int n = wave * kRows + lane / LANES; n - lane / LANES < m; n += kStep * U) {
+    uint4 bv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) bv[u] = ld8h_to(B + (size_t)(n0 + min(n + kStep * u, m - 1)) * r + j, left);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const f32x8 w = widen(bv[u]);
+      float acc = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc = fmaf(mine[e], w[e], acc);
+#pragma unroll
+      for (int off = 1; off < LANES; off *= 2) acc += __shfl_xor(acc, off, 64);
+      if (lane % LANES == 0 && n + kStep * u < m) o[n + kStep * u] = acc;
+    }
+  }
+}
 
 template <bool XBF16, bool YBF16>
 __global__ __launch_bounds__(kTokThreads) void token_kernel(moe_lora L, const void* __restrict__ x,
                                                             const int32_t* __restrict__ ids, const void* base,
                                                             void* out, int per) {
   __shared__ __align__(16) float v[kMaxRank];
+  __shared__ __align__(16) float o[kTokOut];
   const int t = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int id = ids[t];
   const bool has = id >= 0 && id < L.num;
@@ -42,57 +140,51 @@ __global__ __launch_bounds__(kTokThreads) void token_kernel(moe_lora L, const vo
   const uint16_t* A = (const uint16_t*)L.a + (has ? (size_t)id * L.r * L.K : 0);
   const uint16_t* B = (const uint16_t*)L.b + (has ? (size_t)id * L.N * L.r : 0);
   const float scale = has && L.scale ? L.scale[id] : 1.0f;
-  const int K = L.K, n0 = blockIdx.y * per, n1 = min(L.N, n0 + per);
+  const int n0 = blockIdx.y * per, n1 = min(L.N, n0 + per);
   if (threadIdx.x < kMaxRank) v[threadIdx.x] = 0.0f;
   __syncthreads();
-  constexpr int R = 2;  // rows of A a wavefront multiplies at once
-  const int kfull = K & ~511;
-  for (int j = wave * R; j < rank; j += kTokWaves * R) {
-    float acc[R] = {};
-    const uint16_t* row[R];
+  const size_t at = (size_t)t * L.K;
+  if (rank <= 2 * kTokWaves) {
+    if (wave * 2 < rank) {
+      float acc[2];
+      token_rows<XBF16, 2, 4>(x, at, A, wave * 2, rank, L.K, acc);
 #pragma unroll
-    for (int i = 0; i < R; ++i) row[i] = A + (size_t)min(j + i, rank - 1) * K;
-    const size_t at = (size_t)t * K;
-#pragma unroll 4
-    for (int k = lane * 8; k < kfull; k += 512) {
-      const f32x8 xv = load8<XBF16>(x, at + k, 8);
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const f32x8 av = widen(ld8h(row[i] + k));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i] = fmaf(xv[e], av[e], acc[i]);
-      }
+      for (int i = 0; i < 2; ++i)
+        if (lane == 0 && wave * 2 + i < rank) v[wave * 2 + i] = acc[i] * scale;
     }
-    const int k = kfull + lane * 8;
-    if (k < K) {
-      const f32x8 xv = load8<XBF16>(x, at + k, K - k);
+  } else {
+    for (int j = wave * 4; j < rank; j += kTokWaves * 4) {
+      float acc[4];
+      token_rows<XBF16, 4, 4>(x, at, A, j, rank, L.K, acc);
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const f32x8 av = widen(ld8h_to(row[i] + k, K - k));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i] = fmaf(xv[e], av[e], acc[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const float s = wave_sum(acc[i]);
-      if (lane == 0 && j + i < rank) v[j + i] = s * scale;
+      for (int i = 0; i < 4; ++i)
+        if (lane == 0 && j + i < rank) v[j + i] = acc[i] * scale;
     }
   }
   __syncthreads();
-  for (int n = n0 + threadIdx.x; n < n1; n += kTokThreads) {
-    const size_t at = (size_t)t * L.N + n;
-    float acc = 0.f;
-    for (int j = 0; j < rank; j += 8) {
-      const f32x8 bv = widen(ld8h_to(B + (size_t)n * L.r + j, rank - j));
+  for (int n = n0; n < n1; n += kTokOut) {
+    const int m = min(kTokOut, n1 - n);
+    if (rank > 64)
+      token_outputs<16>(B, v, n, m, L.r, rank, o);
+    else if (rank > 32)
+      token_outputs<8>(B, v, n, m, L.r, rank, o);
+    else if (rank > 16)
+      token_outputs<4>(B, v, n, m, L.r, rank, o);
+    else if (rank > 8)
+      token_outputs<2>(B, v, n, m, L.r, rank, o);
+    else if (rank > 0)
+      token_outputs<1>(B, v, n, m, L.r, rank, o);
+    __syncthreads();
+    for (int e = threadIdx.x * 8; e < m; e += kTokThreads * 8) {
+      const size_t to = (size_t)t * L.N + n + e;
+      f32x8 y = base ? load8<YBF16>(base, to, m - e) : f32x8(0.f);
+      if (rank > 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc = fmaf(v[j + e], bv[e], acc);
+        for (int i = 0; i < 8; ++i) y[i] += o[min(e + i, kTokOut - 1)];
+      }
+      store8<YBF16>(out, to, m - e, y);
     }
-    if (base) acc += YBF16 ? bf(((const uint16_t*)base)[at]) : ((const float*)base)[at];
-    if (YBF16)
-      ((uint16_t*)out)[at] = f32_to_bf16(acc);
-    else
-      ((float*)out)[at] = acc;
+    __syncthreads();
   }
 }
 
@@ -101,26 +193,29 @@ __global__ __launch_bounds__(kTokThreads) void token_kernel(moe_lora L, const vo
 // v_mfma_f32_16x16x32_bf16: lane l supplies row (first operand) or column
 // (second) l % 16 at K positions 8 (l / 16) .. + 7, and receives column l % 16,
 // rows 4 (l / 16) .. + 3.  v_mfma_f32_16x16x4_f32: one K position, l / 16.
-// A contraction may take its positions in any order as long as both operands
-// take the same, so a lane reads 16 consecutive elements of its row at a time.
+// Read straight from memory that layout touches a row a lane, sixteen bytes of
+// it, which the cache serves a lane at a time; so every wavefront loads whole
+// lines, eight or more lanes a row, and turns them in a part of LDS that is its
+// own (no barrier; 16-byte pieces XOR-swizzled so that the eight lanes served
+// together fall on different banks).
 //
 // A x: first operand the rows of A (16 of them a "task": one adapter, 16 of its
-// ranks), second the tokens; the wavefronts split K and their parts meet in
-// LDS.  The sum of a token's own adapter is split into bf16 parts whose sum is
-// the fp32 value (two parts, off by at most 2^-16 of it, for bf16 outputs;
-// three, exact, for fp32), so the second product runs on bf16 operands too.
+// ranks), second the tokens; the wavefronts split K in slabs of 64 and their
+// parts meet in LDS.  The sum of a token's own adapter is split into bf16 parts
+// whose sum is the fp32 value (two parts, off by at most 2^-16 of it, for bf16
+// outputs; three, exact, for fp32), so the second product runs on bf16 operands.
 //
-// B v: first operand 16 outputs, second the tokens.  Output row m of product q
-// stands for output 16 (m / 4) + 4 q + m % 4 of a block of 64, so that four
-// products leave 16 consecutive outputs of a token in each lane.  The parts
-// and ranks of v are one list of chunks of eight, four to a product.  Every
-// adapter of the tile has its own sum and a token takes its own adapter's, so
-// one adapter's NaN cannot reach another's tokens.
+// B v: first operand the tokens' parts, second 16 outputs.  Column m of product q
+// stands for output 4 m + q of a block of 64, so that four products leave four
+// consecutive outputs of four tokens in each lane, a line of each token in 16.  B comes in slabs of up
+// to four chunks of eight ranks; the parts of v over them fill a product's four
+// chunks.  Each adapter's product goes to its own tokens only, so one adapter's
+// NaN cannot reach another's tokens.
 
-constexpr int kTileThreads = 512, kTileWaves = kTileThreads / 64;
-constexpr int kPass = 4;                 // tasks per pass over x
-constexpr int kUnroll = 2;               // blocks of K in flight
-constexpr int kVStride = kMaxRank + 8;   // bf16 elements of a token's row of v parts
+constexpr int kTileWaves = 8, kTileThreads = 64 * kTileWaves;
+constexpr int kPass = 4;                // tasks per pass over x
+constexpr int kStage = 12288;           // a wavefront's LDS: x 2 or 4 KB and A 2 KB a task; or a slab of B
+constexpr int kVStride = kMaxRank + 8;  // bf16 elements of a token's row of v parts
 
 // fp32 -> bf16 by truncation: what is left over is exact
 __device__ __forceinline__ uint16_t take_bf16(float& f) {
@@ -130,111 +225,333 @@ __device__ __forceinline__ uint16_t take_bf16(float& f) {
   return (uint16_t)(u >> 16);
 }
 
-// A lane's 16 consecutive outputs of its token, n of them (<= 0: none) inside N.
+// what a wavefront's lanes wrote to its LDS may now be read by its other lanes
+__device__ __forceinline__ void wave_turn() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// four consecutive outputs of a token, n of them (<= 0: none) inside N
 template <bool YBF16>
-struct Out {
-  uint4 h[2];
-  f32x8 f[2];
+struct Four {
+  uint32_t u[YBF16 ? 2 : 4];
 
   __device__ __forceinline__ void load(const void* base, size_t at, int n) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if constexpr (YBF16)
-        h[i] = base ? ld8h_to((const uint16_t*)base + at + 8 * i, n - 8 * i) : make_uint4(0, 0, 0, 0);
-      else
-        f[i] = base ? ld8f_to((const float*)base + at + 8 * i, n - 8 * i) : f32x8(0.f);
+    if constexpr (YBF16) {
+      u[0] = u[1] = 0;
+      if (!base) return;
+      const uint16_t* p = (const uint16_t*)base + at;
+      if (n >= 4) {
+        const Packed4h v = *(const Packed4h*)p;
+        u[0] = v.x, u[1] = v.y;
+      } else {
+        u[0] = ld2h_part(p, n), u[1] = ld2h_part(p + 2, n - 2);
+      }
+    } else {
+      u[0] = u[1] = u[2] = u[3] = 0;
+      if (!base) return;
+      const float* p = (const float*)base + at;
+      if (n >= 4) {
+        const Packed4f v = *(const Packed4f*)p;
+        u[0] = __float_as_uint(v.x), u[1] = __float_as_uint(v.y), u[2] = __float_as_uint(v.z), u[3] = __float_as_uint(v.w);
+      } else {
+        u[0] = __float_as_uint(ld1f_if(p, n > 0)), u[1] = __float_as_uint(ld1f_if(p + 1, n > 1));
+        u[2] = __float_as_uint(ld1f_if(p + 2, n > 2));
+      }
     }
   }
 
-  __device__ __forceinline__ void store(void* out, size_t at, int n, const v4f (&d)[4]) const {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      f32x8 w;
-      if constexpr (YBF16)
-        w = widen(h[i]);
-      else
-        w = f[i];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] += d[2 * i + (e >> 2)][e & 3];
-      store8<YBF16>(out, at + 8 * i, n - 8 * i, w);
+  __device__ __forceinline__ void load_all(const void* base, size_t at) {
+    if constexpr (YBF16) {
+      const Packed4h v = *(const Packed4h*)((const uint16_t*)base + at);
+      u[0] = v.x, u[1] = v.y;
+    } else {
+      const Packed4f v = *(const Packed4f*)((const float*)base + at);
+      u[0] = __float_as_uint(v.x), u[1] = __float_as_uint(v.y), u[2] = __float_as_uint(v.z), u[3] = __float_as_uint(v.w);
+    }
+  }
+
+  // d, and what was loaded if `based`
+  __device__ __forceinline__ void store_all(void* out, size_t at, bool based, v4f d) const {
+    if constexpr (YBF16) {
+      const uint32_t a = based ? u[0] : 0, b = based ? u[1] : 0;
+      d += v4f{bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b)};
+      *(Packed4h*)((uint16_t*)out + at) = Packed4h{pack2(d[0], d[1]), pack2(d[2], d[3])};
+    } else {
+      const v4f b = {__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]), __uint_as_float(u[3])};
+      d = based ? d + b : d;
+      *(Packed4f*)((float*)out + at) = Packed4f{d[0], d[1], d[2], d[3]};
+    }
+  }
+
+  // + d, rounded once
+  __device__ __forceinline__ void store(void* out, size_t at, int n, v4f d) const {
+    if constexpr (YBF16) {
+      d += v4f{bf16_lo(u[0]), bf16_hi(u[0]), bf16_lo(u[1]), bf16_hi(u[1])};
+      uint16_t* p = (uint16_t*)out + at;
+      if (n >= 4) {
+        *(Packed4h*)p = Packed4h{pack2(d[0], d[1]), pack2(d[2], d[3])};
+      } else {
+        if (n > 0) p[0] = f32_to_bf16(d[0]);
+        if (n > 1) p[1] = f32_to_bf16(d[1]);
+        if (n > 2) p[2] = f32_to_bf16(d[2]);
+      }
+    } else {
+      d += v4f{__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]), __uint_as_float(u[3])};
+      float* p = (float*)out + at;
+      if (n >= 4) {
+        *(Packed4f*)p = Packed4f{d[0], d[1], d[2], d[3]};
+      } else {
+        if (n > 0) p[0] = d[0];
+        if (n > 1) p[1] = d[1];
+        if (n > 2) p[2] = d[2];
+      }
     }
   }
 };
 
-// B v of one adapter for the 64 outputs at nb.  FULL: all of them inside N, the
-// rank a multiple of eight.
-template <int NS, bool FULL>
-__device__ __forceinline__ void expand(const uint16_t* __restrict__ B, const uint16_t (&vs)[NS][16][kVStride], int nb,
-                                       int N, int r, int rank, v4f (&d)[4]) {
-  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-  const int c8 = (rank + 7) / 8, chunks = NS * c8;
-  for (int m = 0; m < chunks; m += 4) {
-    const int c = m + g, cc = min(c, chunks - 1), pt = (cc >= c8) + (cc >= 2 * c8), j = (cc - pt * c8) * 8;
-    uint4 vv = *(const uint4*)&vs[pt][col][j], bv[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = nb + (col >> 2) * 16 + q * 4 + (col & 3);
-      bv[q] = FULL ? ld8h(B + (size_t)n * r + j) : ld8h_to(B + (size_t)min(n, N - 1) * r + j, rank - j);
-      if (c >= chunks) bv[q] = make_uint4(0, 0, 0, 0);
-    }
-    if (c >= chunks) vv = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      d[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, bv[q]), __builtin_bit_cast(v8bf, vv),
-                                                     d[q], 0, 0, 0);
-  }
-}
-
-// One block of 64 K positions of NP tasks: this lane's 16 elements at k.  FULL:
-// the block lies inside K.
-template <bool XBF16, int NP, bool FULL>
-__device__ __forceinline__ void shrink_block(const void* __restrict__ xrow, const uint16_t* const (&arow)[kPass], int k,
-                                             int K, v4f (&acc)[kPass]) {
-  if (XBF16) {
-    const uint16_t* xp = (const uint16_t*)xrow + k;
-    uint4 xv[2], av[NP][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) xv[h] = FULL ? ld8h(xp + 8 * h) : ld8h_to(xp + 8 * h, K - k - 8 * h);
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        av[p][h] = FULL ? ld8h(arow[p] + k + 8 * h) : ld8h_to(arow[p] + k + 8 * h, K - k - 8 * h);
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, av[p][h]),
-                                                         __builtin_bit_cast(v8bf, xv[h]), acc[p], 0, 0, 0);
-  } else {
-    const float* xp = (const float*)xrow + k;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x8 xv = FULL ? ld8f(xp + 8 * h) : ld8f_to(xp + 8 * h, K - k - 8 * h);
-      f32x8 av[NP];
-#pragma unroll
-      for (int p = 0; p < NP; ++p)
-        av[p] = widen(FULL ? ld8h(arow[p] + k + 8 * h) : ld8h_to(arow[p] + k + 8 * h, K - k - 8 * h));
-#pragma unroll
-      for (int p = 0; p < NP; ++p)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[p] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[p][e], xv[e], acc[p], 0, 0, 0);
-    }
-  }
-}
-
+// a wavefront's slab of 64 K positions: 16 tokens and NP tasks of 16 ranks
 template <bool XBF16, int NP>
-__device__ __forceinline__ void shrink(const void* __restrict__ xrow, const uint16_t* const (&arow)[kPass], int wave,
-                                       int g, int K, v4f (&acc)[kPass]) {
-  const int full = K / 64;  // whole blocks; block b goes to wavefront b % kTileWaves
-  int b = wave;
-  for (; b + (kUnroll - 1) * kTileWaves < full; b += kUnroll * kTileWaves) {
+struct Slab {
+  static constexpr int kX = XBF16 ? 2 : 4;  // 16-byte pieces of x a lane
+  uint4 x[kX], a[NP][2];
+
+  // pieces of 8 (x fp32: 4) elements; FULL: the slab lies inside K
+  template <bool FULL>
+  __device__ __forceinline__ void load(const void* const (&xrow)[kX], const uint16_t* const (&arow)[kPass][2], int k0,
+                                       int K) {
+    const int lane = threadIdx.x & 63, k8 = k0 + (lane & 7) * 8;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      shrink_block<XBF16, NP, true>(xrow, arow, (b + u * kTileWaves) * 64 + g * 16, K, acc);
+    for (int i = 0; i < kX; ++i) {
+      if constexpr (XBF16) {
+        x[i] = FULL ? ld8h((const uint16_t*)xrow[i] + k8) : ld8h_to((const uint16_t*)xrow[i] + k8, K - k8);
+      } else {
+        const int k4 = k0 + (lane & 15) * 4;
+        const float* f = (const float*)xrow[i] + k4;
+        if (FULL || K - k4 >= 4) {
+          const Packed4f v = *(const Packed4f*)f;
+          x[i] = make_uint4(__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w));
+        } else {
+          x[i] = make_uint4(__float_as_uint(ld1f_if(f, k4 < K)), __float_as_uint(ld1f_if(f + 1, k4 + 1 < K)),
+                            __float_as_uint(ld1f_if(f + 2, k4 + 2 < K)), 0u);
+        }
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) a[p][i] = FULL ? ld8h(arow[p][i] + k8) : ld8h_to(arow[p][i] + k8, K - k8);
   }
-  for (; b < full; b += kTileWaves) shrink_block<XBF16, NP, true>(xrow, arow, b * 64 + g * 16, K, acc);
-  if (b == full && b * 64 < K) shrink_block<XBF16, NP, false>(xrow, arow, b * 64 + g * 16, K, acc);
+
+  __device__ __forceinline__ void multiply(char* lds, v4f (&acc)[kPass]) const {
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4, r8 = lane >> 3, c8 = lane & 7;
+    constexpr int kXBytes = kX * 1024, kRow = XBF16 ? 128 : 256;
+    wave_turn();  // the last slab has been read
+#pragma unroll
+    for (int i = 0; i < kX; ++i) {
+      const int row = XBF16 ? i * 8 + r8 : i * 4 + (lane >> 4), c = XBF16 ? c8 : lane & 15;
+      *(uint4*)(lds + row * kRow + (c ^ (row & 7)) * 16) = x[i];
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = i * 8 + r8;
+        *(uint4*)(lds + kXBytes + p * 2048 + row * 128 + (c8 ^ (row & 7)) * 16) = a[p][i];
+      }
+    wave_turn();
+    const char* xl = lds + col * kRow;
+    const char* al = lds + kXBytes + col * 128;
+    if constexpr (XBF16) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = ((h * 4 + g) ^ (col & 7)) * 16;
+        const v8bf xv = *(const v8bf*)(xl + at);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*(const v8bf*)(al + p * 2048 + at), xv, acc[p], 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int c = h * 4 + g;
+        const v4f xv = *(const v4f*)(xl + (c ^ (col & 7)) * 16);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          const uint2 w = *(const uint2*)(al + p * 2048 + ((c >> 1) ^ (col & 7)) * 16 + (c & 1) * 8);
+          acc[p] = __builtin_amdgcn_mfma_f32_16x16x4f32(bf16_lo(w.x), xv[0], acc[p], 0, 0, 0);
+          acc[p] = __builtin_amdgcn_mfma_f32_16x16x4f32(bf16_hi(w.x), xv[1], acc[p], 0, 0, 0);
+          acc[p] = __builtin_amdgcn_mfma_f32_16x16x4f32(bf16_lo(w.y), xv[2], acc[p], 0, 0, 0);
+          acc[p] = __builtin_amdgcn_mfma_f32_16x16x4f32(bf16_hi(w.y), xv[3], acc[p], 0, 0, 0);
+        }
+      }
+    }
+  }
+};
+
+// A x of NP tasks over this wavefront's slabs (slab b belongs to wavefront
+// b % kTileWaves).  The next slabs' loads are always issued, past the last slab
+// again for the last: with a known number of them in flight the compiler waits
+// for the slab it needs and no more.
+template <bool XBF16, int NP>
+__device__ __forceinline__ void shrink(const void* const (&xrow)[Slab<XBF16, NP>::kX],
+                                       const uint16_t* const (&arow)[kPass][2], int wave, int K, char* lds,
+                                       v4f (&acc)[kPass]) {
+  const int full = K / 64;
+  int b = wave;
+  if (b < full) {
+    const int last = full - 1 - (full - 1 - b) % kTileWaves;
+    Slab<XBF16, NP> s0, s1, s2;
+    s0.template load<true>(xrow, arow, b * 64, K);
+    s1.template load<true>(xrow, arow, min(b + kTileWaves, last) * 64, K);
+    for (; b < full; b += kTileWaves) {
+      if constexpr (XBF16) {
+        s2.template load<true>(xrow, arow, min(b + 2 * kTileWaves, last) * 64, K);
+        s0.multiply(lds, acc);
+        s0 = s1;
+        s1 = s2;
+      } else {  // one ahead: fp32 tokens take twice the registers
+        s0.multiply(lds, acc);
+        s0 = s1;
+        s1.template load<true>(xrow, arow, min(b + 2 * kTileWaves, last) * 64, K);
+      }
+    }
+  }
+  if (b == full && b * 64 < K) {
+    Slab<XBF16, NP> s0;
+    s0.template load<false>(xrow, arow, b * 64, K);
+    s0.multiply(lds, acc);
+  }
+}
+
+// A step of the second product: one adapter's ranks 8 j0 .. + 31
+struct Step {
+  const uint16_t* B;
+  int slot, rank, j0;
+};
+
+// a step from LDS, in scalar registers
+__device__ __forceinline__ Step fetch(const Step* list, int i) {
+  const uint64_t b = (uint64_t)list[i].B;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+  return Step{(const uint16_t*)(((uint64_t)hi << 32) | lo), (int)__builtin_amdgcn_readfirstlane(list[i].slot),
+              (int)__builtin_amdgcn_readfirstlane(list[i].rank), (int)__builtin_amdgcn_readfirstlane(list[i].j0)};
+}
+
+// 64 rows of B (outputs nb ..) of a step, a 16-byte piece a lane and load; ranks
+// behind the adapter's are zero
+struct Pieces {
+  uint4 p[4];
+
+  // the block inside N and r a multiple of eight: loads without a branch
+  __device__ __forceinline__ void load(const Step& s, int nb, int r) {
+    const int lane = threadIdx.x & 63, j = min((s.j0 + (lane & 3)) * 8, r - 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = ld8h(s.B + (size_t)(nb + i * 16 + (lane >> 2)) * r + j);
+  }
+
+  __device__ __forceinline__ void load_part(const Step& s, int nb, int N, int r) {
+    const int lane = threadIdx.x & 63, j = (s.j0 + (lane & 3)) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = ld8h_to(s.B + (size_t)min(nb + i * 16 + (lane >> 2), N - 1) * r + j, s.rank - j);
+  }
+
+  // to LDS: row n of the 64 lies at 16 (n % 4) + n / 4
+  __device__ __forceinline__ void put(const Step& s, char* lds) const {
+    const int lane = threadIdx.x & 63, c = lane & 3, left = s.rank - (s.j0 + c) * 8;
+    const uint32_t m0 = left >= 2 ? ~0u : left == 1 ? 0xffffu : 0u, m1 = left >= 4 ? ~0u : left == 3 ? 0xffffu : 0u,
+                   m2 = left >= 6 ? ~0u : left == 5 ? 0xffffu : 0u, m3 = left >= 8 ? ~0u : left == 7 ? 0xffffu : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = i * 16 + (lane >> 2), m = n >> 2;
+      *(uint4*)(lds + ((n & 3) * 16 + m) * 64 + (c ^ ((m >> 1) & 3)) * 16) =
+          make_uint4(p[i].x & m0, p[i].y & m1, p[i].z & m2, p[i].w & m3);
+    }
+  }
+};
+
+// the products of a step's pieces with the parts of v
+template <int NS>
+__device__ __forceinline__ void multiply(const Step& s, const uint16_t (&vs)[NS][16][kVStride], const char* lds,
+                                         v4f (&d)[4]) {
+  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+  v8bf bv[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) bv[q] = *(const v8bf*)(lds + (q * 16 + col) * 64 + (g ^ ((col >> 1) & 3)) * 16);
+#pragma unroll
+  for (int m = 0; m < NS; ++m) {
+    const v8bf vv = *(const v8bf*)&vs[m][col][(s.j0 + g) * 8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) d[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, bv[q], d[q], 0, 0, 0);
+  }
+}
+
+// a step's result to its own tokens: acc takes d where the token's slot is the step's
+__device__ __forceinline__ void take(const Step& s, const int (&slot)[4], const v4f (&d)[4], v4f (&acc)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[q][i] = slot[i] == s.slot ? d[q][i] : acc[q][i];
+}
+
+template <bool YBF16>
+__device__ __forceinline__ void load_base(Four<YBF16> (&y)[4], const void* base, const size_t (&row)[4], int n) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i].load_all(base, row[i] + n);
+}
+
+template <bool YBF16>
+__device__ __forceinline__ void store_sum(const Four<YBF16> (&y)[4], bool based, void* out, const size_t (&row)[4],
+                                          int n, const v4f (&acc)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i].store_all(out, row[i] + n, based, v4f{acc[0][i], acc[1][i], acc[2][i], acc[3][i]});
+}
+
+// The second product over whole blocks of 64 outputs, every kTileWaves-th from nb
+// to n1, `steps` steps each, G at a time.  All loads and stores of a block are
+// unconditional, so the pieces of the next G steps (fetched as soon as the last
+// have gone to LDS) and the next block's base stay in flight meanwhile.
+template <int NS, bool YBF16, int G>
+__device__ __forceinline__ void blocks(const moe_lora& L, const Step* list, int steps, const int (&slot)[4],
+                                       const size_t (&row)[4], const uint16_t (&vs)[NS][16][kVStride], int nb, int n1,
+                                       const void* base, bool based, void* out, char* lds) {
+  if (nb >= n1) return;
+  const int n = (threadIdx.x & 15) * 4, r = L.r;
+  Four<YBF16> y[4], y_next[4];
+  Pieces p[G];
+  load_base(y, base, row, nb + n);
+#pragma unroll
+  for (int g = 0; g < G; ++g) p[g].load(fetch(list, min(g, steps - 1)), nb, r);
+  for (; nb < n1; nb += kTileWaves * 64) {
+    const int nb2 = nb + kTileWaves * 64 < n1 ? nb + kTileWaves * 64 : nb;
+    v4f acc[4] = {}, d[4] = {};
+    load_base(y_next, base, row, nb2 + n);
+    for (int u = 0; u < steps; u += G) {
+      const bool end = u + G >= steps;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const Step s = fetch(list, min(u + g, steps - 1));
+        const Step after = fetch(list, end ? min(g, steps - 1) : min(u + G + g, steps - 1));
+        wave_turn();  // the last pieces have been read
+        p[g].put(s, lds);
+        wave_turn();
+        p[g].load(after, end ? nb2 : nb, r);
+        if (u + g < steps) {  // no memory but LDS in here
+          if (s.j0 == 0) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) d[q] = v4f{0.f, 0.f, 0.f, 0.f};
+          }
+          multiply<NS>(s, vs, lds, d);
+          take(s, slot, d, acc);
+        }
+      }
+    }
+    store_sum(y, based, out, row, nb + n, acc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = y_next[i];
+  }
 }
 
 template <bool XBF16, bool YBF16>
@@ -242,71 +559,87 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
                                                             const int32_t* __restrict__ ids, const void* base,
                                                             void* out, int per) {
   constexpr int NS = YBF16 ? 2 : 3;
-  __shared__ __align__(16) float part[kTileWaves][kPass][16][16];  // [wave][task][token][rank]
+  __shared__ __align__(16) char stage[kTileWaves][kStage];
   __shared__ __align__(16) uint16_t vs[NS][16][kVStride];
-  __shared__ int tok_slot[16], ad_id[16], ad_rank[16], n_ad, n_task;
+  __shared__ int tok_slot[16], ad_id[16], ad_rank[16], n_task, n_step;
   __shared__ uint8_t task_slot[128], task_tile[128];
+  __shared__ Step step[64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
   const int t0 = blockIdx.x * 16, K = L.K, N = L.N, r = L.r;
+  char* lds = stage[wave];
 
+  // the tile's distinct adapters and their tasks
   if (wave == 0) {
-    const int id = lane < 16 && t0 + lane < T ? ids[t0 + lane] : -1;
+    const int id = lane < 16 ? ids[min(t0 + lane, T - 1)] : -1;  // past the end: the last token again
     const bool has = lane < 16 && id >= 0 && id < L.num;
-    int lead = lane;
+    int lead = lane;  // the first of the tokens with this id
+#pragma unroll
     for (int i = 15; i >= 0; --i)
-      if (__shfl(id, i, 64) == id) lead = i;
+      if (__builtin_amdgcn_readlane(id, i) == id) lead = i;
     const uint64_t leads = __ballot(has && lead == lane);
-    const uint64_t before = (1ull << lane) - 1;
-    const int rank = has ? rank_of(L, id) : 0;
-    int at = 0;  // tasks of the adapters before this one
-    const int tiles = (rank + 15) / 16;
+    const int rank = has ? rank_of(L, id) : 0, tiles = (rank + 15) / 16;
+    const int slabs = (rank + 31) / 32;
+    int at = 0, total = 0, step_at = 0, steps = 0;
+#pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int ti = __shfl(tiles, i, 64);
-      if (((leads >> i) & 1) && i < lane) at += ti;
+      const int ti = ((leads >> i) & 1) ? __builtin_amdgcn_readlane(tiles, i) : 0;
+      const int si = ((leads >> i) & 1) ? __builtin_amdgcn_readlane(slabs, i) : 0;
+      at += i < lane ? ti : 0;
+      step_at += i < lane ? si : 0;
+      total += ti;
+      steps += si;
     }
     if (lane < 16) tok_slot[lane] = has ? __popcll(leads & ((1ull << lead) - 1)) : -1;
     if ((leads >> lane) & 1) {
-      const int slot = __popcll(leads & before);
+      const int slot = __popcll(leads & ((1ull << lane) - 1));
       ad_id[slot] = id;
       ad_rank[slot] = rank;
       for (int i = 0; i < tiles; ++i) task_slot[at + i] = (uint8_t)slot, task_tile[at + i] = (uint8_t)i;
+      const uint16_t* B = (const uint16_t*)L.b + (size_t)id * N * r;
+      for (int i = 0; i < slabs; ++i) step[step_at + i] = Step{B, slot, rank, i * 4};
     }
-    int total = 0;
-    for (int i = 0; i < 16; ++i) {
-      const int ti = __shfl(tiles, i, 64);
-      if ((leads >> i) & 1) total += ti;
-    }
-    if (lane == 0) n_ad = __popcll(leads), n_task = total;
+    if (lane == 0) n_task = total, n_step = steps;
   }
+  for (int i = threadIdx.x; i < (int)sizeof(vs) / 4; i += kTileThreads) ((uint32_t*)vs)[i] = 0;
   __syncthreads();
-  const int ntask = n_task, nad = n_ad;
+  const int ntask = __builtin_amdgcn_readfirstlane(n_task), steps = __builtin_amdgcn_readfirstlane(n_step);
 
   // A x, kPass tasks at a time
-  const char* xrow = (const char*)x + (size_t)min(t0 + col, T - 1) * K * (XBF16 ? 2 : 4);
+  constexpr int kX = XBF16 ? 2 : 4;
+  const void* xrow[kX];
+#pragma unroll
+  for (int i = 0; i < kX; ++i) {
+    const size_t row = (size_t)min(t0 + (XBF16 ? i * 8 + (lane >> 3) : i * 4 + (lane >> 4)), T - 1) * K;
+    xrow[i] = XBF16 ? (const void*)((const uint16_t*)x + row) : (const void*)((const float*)x + row);
+  }
   for (int p0 = 0; p0 < ntask; p0 += kPass) {
     v4f acc[kPass] = {};
-    const uint16_t* arow[kPass];
+    const uint16_t* arow[kPass][2];
 #pragma unroll
-    for (int p = 0; p < kPass; ++p) {
-      const int q = min(p0 + p, ntask - 1), slot = task_slot[q];
-      arow[p] = (const uint16_t*)L.a + ((size_t)ad_id[slot] * r + min(task_tile[q] * 16 + col, ad_rank[slot] - 1)) * K;
-    }
+    for (int p = 0; p < kPass; ++p)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int q = min(p0 + p, ntask - 1), slot = task_slot[q];
+        const int j = min(task_tile[q] * 16 + i * 8 + (lane >> 3), ad_rank[slot] - 1);
+        arow[p][i] = (const uint16_t*)L.a + ((size_t)ad_id[slot] * r + j) * K;
+      }
     const int np = min(kPass, ntask - p0);
     if (np == 1)
-      shrink<XBF16, 1>(xrow, arow, wave, g, K, acc);
+      shrink<XBF16, 1>(xrow, arow, wave, K, lds, acc);
     else if (np == 2)
-      shrink<XBF16, 2>(xrow, arow, wave, g, K, acc);
+      shrink<XBF16, 2>(xrow, arow, wave, K, lds, acc);
     else
-      shrink<XBF16, kPass>(xrow, arow, wave, g, K, acc);
+      shrink<XBF16, kPass>(xrow, arow, wave, K, lds, acc);
+    wave_turn();
 #pragma unroll
-    for (int p = 0; p < kPass; ++p) *(v4f*)&part[wave][p][col][g * 4] = acc[p];
+    for (int p = 0; p < kPass; ++p) *(v4f*)(lds + ((p * 16 + col) * 16 + g * 4) * 4) = acc[p];
     __syncthreads();
     for (int i = threadIdx.x; i < np * 256; i += kTileThreads) {
       const int p = i >> 8, tok = (i >> 4) & 15, rk = i & 15, q = p0 + p, slot = task_slot[q];
       if (tok_slot[tok] == slot) {
         float s = 0.f;
 #pragma unroll
-        for (int wv = 0; wv < kTileWaves; ++wv) s += part[wv][p][tok][rk];
+        for (int wv = 0; wv < kTileWaves; ++wv) s += ((const float*)stage[wv])[i];
         const int j = task_tile[q] * 16 + rk;
         if (L.scale) s *= L.scale[ad_id[slot]];
         if (j >= ad_rank[slot]) s = 0.f;
@@ -317,35 +650,58 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
     __syncthreads();
   }
 
-  // B v and the base, a block of 64 outputs a wavefront at a time
-  const int n0 = blockIdx.y * per, n1 = min(N, n0 + per), myslot = tok_slot[col], t = t0 + col;
-  bool whole = r % 8 == 0;  // no adapter of the tile ends inside a chunk of eight ranks
-  for (int s = 0; s < nad; ++s) whole = whole && ad_rank[s] % 8 == 0;
-  for (int nb = n0 + wave * 64; nb < n1; nb += kTileWaves * 64) {
-    const bool inside = nb + 64 <= N;
-    const size_t at = (size_t)min(t, T - 1) * N + nb + g * 16;
-    Out<YBF16> y;
-    y.load(base, at, inside ? 16 : N - nb - g * 16);
-    v4f acc[4] = {};
-    for (int s = 0; s < nad; ++s) {
-      v4f d[4] = {};
-      const uint16_t* B = (const uint16_t*)L.b + (size_t)ad_id[s] * N * r;
-      if (inside && whole)
-        expand<NS, true>(B, vs, nb, N, r, ad_rank[s], d);
-      else
-        expand<NS, false>(B, vs, nb, N, r, ad_rank[s], d);
-      if (s == myslot) {
+  // B v and the base, a block of 64 outputs a wavefront at a time; a lane has
+  // four outputs of the four tokens 4 g .. + 3.  Rows past the last token repeat
+  // it, its stores too.
+  int slot[4];
+  size_t row[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[q] = d[q];
+  for (int i = 0; i < 4; ++i) {
+    slot[i] = tok_slot[g * 4 + i];
+    row[i] = (size_t)min(t0 + g * 4 + i, T - 1) * N;
+  }
+  const int n1 = min(N, ((int)blockIdx.y + 1) * per);
+  int nb = blockIdx.y * per + wave * 64;
+  const bool based = base != nullptr;
+  if (steps > 0 && r % 8 == 0) {
+    const int whole = n1 / 64 * 64;  // per is a multiple of 64
+    const void* from = based ? base : out;
+    if (steps == 1)
+      blocks<NS, YBF16, 1>(L, step, steps, slot, row, vs, nb, whole, from, based, out, lds);
+    else if (steps == 2)
+      blocks<NS, YBF16, 2>(L, step, steps, slot, row, vs, nb, whole, from, based, out, lds);
+    else
+      blocks<NS, YBF16, 4>(L, step, steps, slot, row, vs, nb, whole, from, based, out, lds);
+    if (nb < whole) nb += (whole - nb + kTileWaves * 64 - 1) / (kTileWaves * 64) * (kTileWaves * 64);
+  }
+  for (; nb < n1; nb += kTileWaves * 64) {
+    Four<YBF16> y[4];
+    v4f acc[4] = {}, d[4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i].load(base, row[i] + nb + col * 4, N - nb - col * 4);
+    for (int u = 0; u < steps; ++u) {
+      const Step s = fetch(step, u);
+      Pieces p;
+      p.load_part(s, nb, N, r);
+      wave_turn();
+      p.put(s, lds);
+      wave_turn();
+      if (s.j0 == 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) d[q] = v4f{0.f, 0.f, 0.f, 0.f};
       }
+      multiply<NS>(s, vs, lds, d);
+      take(s, slot, d, acc);
     }
-    if (t < T) y.store(out, at, inside ? 16 : N - nb - g * 16, acc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      y[i].store(out, row[i] + nb + col * 4, N - nb - col * 4, v4f{acc[0][i], acc[1][i], acc[2][i], acc[3][i]});
   }
 }
 
 template <bool XBF16, bool YBF16>
 void run(const moe_lora* L, const void* x, int T, const int32_t* ids, const void* base, void* out, hipStream_t s) {
-  constexpr int kTokens = 128, kGroups = 256;
+  constexpr int kTokens = KT, kGroups = KG;
   if (T <= kTokens) {
     const int split = max(1, min(kGroups / T, (L->N + 127) / 128));
     const int per = ((L->N + split - 1) / split + 63) / 64 * 64;
@@ -353,7 +709,7 @@ void run(const moe_lora* L, const void* x, int T, const int32_t* ids, const void
            ids, base, out, per);
   } else {
     const int tiles = (T + 15) / 16;
-    const int split = max(1, min((kGroups + tiles - 1) / tiles, (L->N + 64 * kTileWaves - 1) / (64 * kTileWaves)));
+    const int split = max(1, min((kGroups + tiles - 1) / tiles, (L->N + 63) / 64));
     const int per = ((L->N + split - 1) / split + 63) / 64 * 64;
     launch(MOE_PROF_LORA, tile_kernel<XBF16, YBF16>, dim3(tiles, (L->N + per - 1) / per), dim3(kTileThreads), 0, s, *L,
            x, T, ids, base, out, per);
