@@ -62,6 +62,28 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return (uint32_t)f32_to_bf16(lo) | ((uint32_t)f32_to_bf16(hi) << 16);
 }
 
+// Stores of results that this kernel does not read again: they leave the L2 as
+// they come instead of at the kernel's end, when all dirty lines are written back.
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+#ifdef NONT
+#define __builtin_nontemporal_store(v, p) (*(p) = (v))
+#endif
+
+__device__ __forceinline__ void stream4h(uint16_t* p, uint2 v) {
+  __builtin_nontemporal_store(u32x2_any{v.x, v.y}, (u32x2_any*)p);
+}
+
+__device__ __forceinline__ void stream8h(uint16_t* p, uint4 v) {
+  __builtin_nontemporal_store(u32x4_any{v.x, v.y, v.z, v.w}, (u32x4_any*)p);
+}
+
+__device__ __forceinline__ void stream4f(float* p, f32x4 v) {
+  __builtin_nontemporal_store(f32x4_any{v[0], v[1], v[2], v[3]}, (f32x4_any*)p);
+}
+
 template <bool BF16>
 __device__ __forceinline__ f32x8 load8(const void* p, size_t at, int n) {
   if constexpr (BF16)
@@ -70,12 +92,16 @@ __device__ __forceinline__ f32x8 load8(const void* p, size_t at, int n) {
     return ld8f_to((const float*)p + at, n);
 }
 
-template <bool BF16>
+template <bool BF16, bool STREAM = false>
 __device__ __forceinline__ void store8(void* p, size_t at, int n, f32x8 v) {
-  if (BF16) {
+  if constexpr (BF16) {
     uint16_t* o = (uint16_t*)p + at;
     if (n >= 8) {
-      st8h(o, make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])));
+      const uint4 h = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+      if constexpr (STREAM)
+        stream8h(o, h);
+      else
+        st8h(o, h);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -84,8 +110,13 @@ __device__ __forceinline__ void store8(void* p, size_t at, int n, f32x8 v) {
   } else {
     float* o = (float*)p + at;
     if (n >= 8) {
-      *(Packed4f*)o = Packed4f{v[0], v[1], v[2], v[3]};
-      *(Packed4f*)(o + 4) = Packed4f{v[4], v[5], v[6], v[7]};
+      if constexpr (STREAM) {
+        stream4f(o, f32x4{v[0], v[1], v[2], v[3]});
+        stream4f(o + 4, f32x4{v[4], v[5], v[6], v[7]});
+      } else {
+        *(Packed4f*)o = Packed4f{v[0], v[1], v[2], v[3]};
+        *(Packed4f*)(o + 4) = Packed4f{v[4], v[5], v[6], v[7]};
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)

@@ -277,11 +277,11 @@ struct Four {
     if constexpr (YBF16) {
       const uint32_t a = based ? u[0] : 0, b = based ? u[1] : 0;
       d += v4f{bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b)};
-      *(Packed4h*)((uint16_t*)out + at) = Packed4h{pack2(d[0], d[1]), pack2(d[2], d[3])};
+      stream4h((uint16_t*)out + at, make_uint2(pack2(d[0], d[1]), pack2(d[2], d[3])));
     } else {
       const v4f b = {__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]), __uint_as_float(u[3])};
       d = based ? d + b : d;
-      *(Packed4f*)((float*)out + at) = Packed4f{d[0], d[1], d[2], d[3]};
+      stream4f((float*)out + at, d);
     }
   }
 
@@ -319,8 +319,7 @@ struct Slab {
 
   // pieces of 8 (x fp32: 4) elements; FULL: the slab lies inside K
   template <bool FULL>
-  __device__ __forceinline__ void load(const void* const (&xrow)[kX], const uint16_t* const (&arow)[kPass][2], int k0,
-                                       int K) {
+  __device__ __forceinline__ void load_x(const void* const (&xrow)[kX], int k0, int K) {
     const int lane = threadIdx.x & 63, k8 = k0 + (lane & 7) * 8;
 #pragma unroll
     for (int i = 0; i < kX; ++i) {
@@ -338,10 +337,22 @@ struct Slab {
         }
       }
     }
+  }
+
+  template <bool FULL>
+  __device__ __forceinline__ void load_a(const uint16_t* const (&arow)[kPass][2], int k0, int K) {
+    const int k8 = k0 + (threadIdx.x & 7) * 8;
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
       for (int i = 0; i < 2; ++i) a[p][i] = FULL ? ld8h(arow[p][i] + k8) : ld8h_to(arow[p][i] + k8, K - k8);
+  }
+
+  template <bool FULL>
+  __device__ __forceinline__ void load(const void* const (&xrow)[kX], const uint16_t* const (&arow)[kPass][2], int k0,
+                                       int K) {
+    load_x<FULL>(xrow, k0, K);
+    load_a<FULL>(arow, k0, K);
   }
 
   __device__ __forceinline__ void multiply(char* lds, v4f (&acc)[kPass]) const {
@@ -562,6 +573,7 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
   __shared__ __align__(16) char stage[kTileWaves][kStage];
   __shared__ __align__(16) uint16_t vs[NS][16][kVStride];
   __shared__ int tok_slot[16], ad_id[16], ad_rank[16], n_task, n_step;
+  __shared__ float ad_scale[16];
   __shared__ uint8_t task_slot[128], task_tile[128];
   __shared__ Step step[64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
@@ -594,6 +606,7 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
       const int slot = __popcll(leads & ((1ull << lane) - 1));
       ad_id[slot] = id;
       ad_rank[slot] = rank;
+      ad_scale[slot] = L.scale ? L.scale[id] : 1.0f;
       for (int i = 0; i < tiles; ++i) task_slot[at + i] = (uint8_t)slot, task_tile[at + i] = (uint8_t)i;
       const uint16_t* B = (const uint16_t*)L.b + (size_t)id * N * r;
       for (int i = 0; i < slabs; ++i) step[step_at + i] = Step{B, slot, rank, i * 4};
@@ -641,7 +654,7 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
 #pragma unroll
         for (int wv = 0; wv < kTileWaves; ++wv) s += ((const float*)stage[wv])[i];
         const int j = task_tile[q] * 16 + rk;
-        if (L.scale) s *= L.scale[ad_id[slot]];
+        s *= ad_scale[slot];
         if (j >= ad_rank[slot]) s = 0.f;
 #pragma unroll
         for (int n = 0; n < NS; ++n) vs[n][tok][j] = take_bf16(s);

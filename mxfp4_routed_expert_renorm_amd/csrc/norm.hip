@@ -60,7 +60,7 @@ __global__ __launch_bounds__(1024) void norm_in_kernel(NormArgs a) {
     const int e = (i * a.per_row + in_row) * 8;
     f32x8 o = x[i] * rs;
     if (a.pre_w) o *= a.next_offset + widen_raw(w[i], a.nwbf);
-    store8<OBF16>(a.next_out, at + e, a.H - e, o);
+    store8<OBF16, V == 2>(a.next_out, at + e, a.H - e, o);
   }
 }
 
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(1024) void norm_out_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = (i * a.per_row + in_row) * 8;
-      store8<RBF16>(a.out, at + e, a.H - e, r[i]);
+      store8<RBF16, V == 2>(a.out, at + e, a.H - e, r[i]);
     }
   }
   if (!a.next_out) return;
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(1024) void norm_out_kernel(NormArgs a) {
     const int e = (i * a.per_row + in_row) * 8;
     r[i] *= rs;
     if (a.pre_w) r[i] *= a.next_offset + widen_raw(nw[i], a.nwbf);
-    store8<NBF16>(a.next_out, at + e, a.H - e, r[i]);
+    store8<NBF16, V == 2>(a.next_out, at + e, a.H - e, r[i]);
   }
 }
 
