@@ -8,5 +8,6 @@ inputs."""
 def __getattr__(name):
     if name == "lib":
         from . import binding
+        globals()["lib"] = binding  # the next access is a plain attribute
         return binding
     raise AttributeError(name)

@@ -264,15 +264,15 @@ def moe_group_wide(keys, nkeys, counts, offsets, perm, scratch, stream=None):
 
 def _ptr(name, what, t, shape, dtypes, dev):
     """The address of a dense GPU tensor of this shape and one of these types."""
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: {what} is {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: {what} must be dense (row-major, contiguous)")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: {what} is on {t.device}, not on cuda:{dev}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: {what} is on {t.device}, not on cuda:{dev}")
 
 
 def _current(name, t):

@@ -68,9 +68,6 @@ typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-#ifdef NONT
-#define __builtin_nontemporal_store(v, p) (*(p) = (v))
-#endif
 
 __device__ __forceinline__ void stream4h(uint16_t* p, uint2 v) {
   __builtin_nontemporal_store(u32x2_any{v.x, v.y}, (u32x2_any*)p);
