@@ -35,9 +35,11 @@ __device__ __forceinline__ int rank_of(const moe_lora& L, int id) {
 // ------------------------------------------------------------ a token a workgroup
 //
 // A x: a wavefront takes R rows of A at a time, a lane eight K positions of each
-// at a stride of 512; R and the steps in flight keep 20 16-byte loads of a
-// wavefront outstanding.  B v: 1 to 16 lanes share a row of B, each with its
-// eight ranks of v in registers, so that a wavefront's loads are contiguous.
+// at a stride of 512, S such steps in flight.  B v: LANES lanes share a row of B,
+// each with its eight ranks of v in registers, so that a wavefront's loads are
+// contiguous.  The first rows of B and the base do not depend on A x and are
+// requested before it: what is left is a chain of the id, the adapter's rank, A
+// and the reductions.
 
 constexpr int kTokThreads = 512, kTokWaves = kTokThreads / 64;
 constexpr int kTokOut = 1024;  // outputs gathered in LDS before they are written
@@ -100,91 +102,107 @@ __device__ __forceinline__ void token_rows(const void* __restrict__ x, size_t at
   for (int i = 0; i < R; ++i) acc[i] = wave_sum(acc[i]);
 }
 
-// B v for the outputs n0 + wave .. of this workgroup's m into o, LANES lanes a row
-template <int LANES>
-__device__ __forceinline__ void token_outputs(const uint16_t* __restrict__ B, const float* v, int n0, int m, int r,
-                                              int rank, float* o) {
-  constexpr int kRows = 64 / LANES, kStep = kTokWaves * kRows, U = 4;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = (lane % LANES) * 8;
-  const int left = rank - j;  // <= 0: this lane has no ranks
+template <bool XBF16, bool YBF16, int LANES, int R, int S>
+__device__ __forceinline__ void token_body(const moe_lora& L, const void* __restrict__ x, int t, int rank, float scale,
+                                           const uint16_t* __restrict__ A, const uint16_t* __restrict__ B,
+                                           const void* base, void* out, int n0, int n1, float* v, float* o) {
+  constexpr int kRows = 64 / LANES, kStep = kTokWaves * kRows, U = 8;  // rows of B a wavefront, a workgroup loads at once
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = L.r, part = (lane % LANES) * 8;
+  const size_t yt = (size_t)t * L.N;
+  auto load_rows = [&](uint4(&bv)[U], int at) {  // rows at .. of this workgroup's outputs, past the last one again
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      bv[u] = ld8h_to(B + (size_t)min(at + wave * kRows + lane / LANES + kStep * u, n1 - 1) * r + part, rank - part);
+  };
+  auto load_y = [&](float(&y)[2], int n) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = n + threadIdx.x + i * kTokThreads;
+      y[i] = base && e < n1 ? load1(base, YBF16, yt + e) : 0.f;
+    }
+  };
+  uint4 bv[U];
+  float y[2];
+  load_rows(bv, n0);
+  load_y(y, n0);
+  for (int j = wave * R; j < rank; j += kTokWaves * R) {
+    float acc[R];
+    token_rows<XBF16, R, S>(x, (size_t)t * L.K, A, j, rank, L.K, acc);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (lane == 0 && j + i < rank) v[j + i] = acc[i] * scale;
+  }
+  __syncthreads();
   f32x8 mine;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) mine[e] = v[min(j + e, kMaxRank - 1)];
-  for (int n = wave * kRows + lane / LANES; n - lane / LANES < m; n += kStep * U) {
-    uint4 bv[U];
+  for (int e = 0; e < 8; ++e) mine[e] = part + e < rank ? v[part + e] : 0.f;
+  for (int n = n0; n < n1; n += kTokOut) {
+    const int m = min(kTokOut, n1 - n);
+    for (int at = 0; at < m; at += kStep * U) {
+      if (n + at != n0) load_rows(bv, n + at);
 #pragma unroll
-    for (int u = 0; u < U; ++u) bv[u] = ld8h_to(B + (size_t)(n0 + min(n + kStep * u, m - 1)) * r + j, left);
+      for (int u = 0; u < U; ++u) {
+        const f32x8 w = widen(bv[u]);
+        float acc = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const f32x8 w = widen(bv[u]);
-      float acc = 0.f;
+        for (int e = 0; e < 8; ++e) acc = fmaf(mine[e], w[e], acc);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc = fmaf(mine[e], w[e], acc);
-#pragma unroll
-      for (int off = 1; off < LANES; off *= 2) acc += __shfl_xor(acc, off, 64);
-      if (lane % LANES == 0 && n + kStep * u < m) o[n + kStep * u] = acc;
+        for (int off = 1; off < LANES; off *= 2) acc += __shfl_xor(acc, off, 64);
+        const int at_u = at + wave * kRows + lane / LANES + kStep * u;
+        if (lane % LANES == 0 && at_u < m) o[at_u] = acc;
+      }
     }
+    __syncthreads();
+    if (n != n0) load_y(y, n);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = threadIdx.x + i * kTokThreads;
+      if (e < m) {
+        if constexpr (YBF16)
+          ((uint16_t*)out)[yt + n + e] = f32_to_bf16(y[i] + o[e]);
+        else
+          ((float*)out)[yt + n + e] = y[i] + o[e];
+      }
+    }
+    __syncthreads();
   }
 }
 
-template <bool XBF16, bool YBF16>
+// WIDE: banks of ranks over 16
+template <bool XBF16, bool YBF16, bool WIDE>
 __global__ __launch_bounds__(kTokThreads) void token_kernel(moe_lora L, const void* __restrict__ x,
                                                             const int32_t* __restrict__ ids, const void* base,
                                                             void* out, int per) {
   __shared__ __align__(16) float v[kMaxRank];
   __shared__ __align__(16) float o[kTokOut];
-  const int t = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int id = ids[t];
+  constexpr int S = XBF16 ? 8 : 4;
+  const int t = blockIdx.x, id = ids[t];
   const bool has = id >= 0 && id < L.num;
   const int rank = has ? rank_of(L, id) : 0;
+  const float scale = has && L.scale ? L.scale[id] : 1.0f;
   const uint16_t* A = (const uint16_t*)L.a + (has ? (size_t)id * L.r * L.K : 0);
   const uint16_t* B = (const uint16_t*)L.b + (has ? (size_t)id * L.N * L.r : 0);
-  const float scale = has && L.scale ? L.scale[id] : 1.0f;
   const int n0 = blockIdx.y * per, n1 = min(L.N, n0 + per);
-  if (threadIdx.x < kMaxRank) v[threadIdx.x] = 0.0f;
-  __syncthreads();
-  const size_t at = (size_t)t * L.K;
-  if (rank <= 2 * kTokWaves) {
-    if (wave * 2 < rank) {
-      float acc[2];
-      token_rows<XBF16, 2, 4>(x, at, A, wave * 2, rank, L.K, acc);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (lane == 0 && wave * 2 + i < rank) v[wave * 2 + i] = acc[i] * scale;
+  if (rank == 0) {
+    if (out == base) return;
+    for (int e = n0 + threadIdx.x; e < n1; e += kTokThreads) {
+      const size_t to = (size_t)t * L.N + e;
+      if constexpr (YBF16)
+        ((uint16_t*)out)[to] = base ? ((const uint16_t*)base)[to] : 0;
+      else
+        ((float*)out)[to] = base ? ((const float*)base)[to] : 0.f;
     }
-  } else {
-    for (int j = wave * 4; j < rank; j += kTokWaves * 4) {
-      float acc[4];
-      token_rows<XBF16, 4, 4>(x, at, A, j, rank, L.K, acc);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lane == 0 && j + i < rank) v[j + i] = acc[i] * scale;
-    }
-  }
-  __syncthreads();
-  for (int n = n0; n < n1; n += kTokOut) {
-    const int m = min(kTokOut, n1 - n);
-    if (rank > 64)
-      token_outputs<16>(B, v, n, m, L.r, rank, o);
-    else if (rank > 32)
-      token_outputs<8>(B, v, n, m, L.r, rank, o);
-    else if (rank > 16)
-      token_outputs<4>(B, v, n, m, L.r, rank, o);
-    else if (rank > 8)
-      token_outputs<2>(B, v, n, m, L.r, rank, o);
-    else if (rank > 0)
-      token_outputs<1>(B, v, n, m, L.r, rank, o);
-    __syncthreads();
-    for (int e = threadIdx.x * 8; e < m; e += kTokThreads * 8) {
-      const size_t to = (size_t)t * L.N + n + e;
-      f32x8 y = base ? load8<YBF16>(base, to, m - e) : f32x8(0.f);
-      if (rank > 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] += o[min(e + i, kTokOut - 1)];
-      }
-      store8<YBF16>(out, to, m - e, y);
-    }
-    __syncthreads();
+  } else if (rank <= 8) {
+    token_body<XBF16, YBF16, 1, 1, 8>(L, x, t, rank, scale, A, B, base, out, n0, n1, v, o);
+  } else if (rank <= 16) {
+    token_body<XBF16, YBF16, 2, 2, S>(L, x, t, rank, scale, A, B, base, out, n0, n1, v, o);
+  } else if constexpr (WIDE) {
+    if (rank <= 32)
+      token_body<XBF16, YBF16, 4, 4, 4>(L, x, t, rank, scale, A, B, base, out, n0, n1, v, o);
+    else if (rank <= 64)
+      token_body<XBF16, YBF16, 8, 4, S>(L, x, t, rank, scale, A, B, base, out, n0, n1, v, o);
+    else
+      token_body<XBF16, YBF16, 16, 4, S>(L, x, t, rank, scale, A, B, base, out, n0, n1, v, o);
   }
 }
 
@@ -718,8 +736,8 @@ void run(const moe_lora* L, const void* x, int T, const int32_t* ids, const void
   if (T <= kTokens) {
     const int split = max(1, min(kGroups / T, (L->N + 127) / 128));
     const int per = ((L->N + split - 1) / split + 63) / 64 * 64;
-    launch(MOE_PROF_LORA, token_kernel<XBF16, YBF16>, dim3(T, (L->N + per - 1) / per), dim3(kTokThreads), 0, s, *L, x,
-           ids, base, out, per);
+    auto* kernel = L->r > 16 ? token_kernel<XBF16, YBF16, true> : token_kernel<XBF16, YBF16, false>;
+    launch(MOE_PROF_LORA, kernel, dim3(T, (L->N + per - 1) / per), dim3(kTokThreads), 0, s, *L, x, ids, base, out, per);
   } else {
     const int tiles = (T + 15) / 16;
     const int split = max(1, min((kGroups + tiles - 1) / tiles, (L->N + 63) / 64));
