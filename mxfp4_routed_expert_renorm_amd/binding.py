@@ -280,7 +280,7 @@ def _current(name, t):
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name}: tensors must be on the GPU")
-    now = _torch().cuda.current_device()
+    now = _torch()._C._cuda_getDevice()
     if dev != now:
         raise ValueError(f"{name}: the tensors are on cuda:{dev}, the current device is cuda:{now}")
     return dev
