@@ -11,6 +11,8 @@
 // Both compute A x whole in every workgroup that needs it (from the caches
 // after the first) and split the outputs over workgroups, so the call is one
 // launch and needs no workspace.
+#include <type_traits>
+
 #include "chunk_dev.h"
 
 namespace moe {
@@ -251,8 +253,7 @@ __global__ __launch_bounds__(kTokThreads, WIDE ? 2 : 4) void token_kernel(moe_lo
 // NaN cannot reach another's tokens.
 
 constexpr int kTileWaves = 8, kTileThreads = 64 * kTileWaves;
-constexpr int kPass = 4;                // tasks per pass over x
-constexpr int kStage = 14336;           // a wavefront's LDS: x 2 or 6 KB and A 2 KB a task; or a slab of B
+constexpr int kMaxPass = 8;             // most tasks per pass over x
 constexpr int kVStride = kMaxRank + 8;  // bf16 elements of a token's row of v parts
 
 // fp32 -> bf16 by truncation: what is left over is exact
@@ -400,18 +401,27 @@ struct XSlab {
   }
 };
 
+// where a lane's two rows of each of a pass's tasks are: the adapter's A, bytes from there
+struct ARows {
+  const char* base[kMaxPass];
+  uint32_t off[kMaxPass][2];
+};
+
 // the same positions of NP tasks of 16 ranks
 template <int NP>
 struct ASlab {
   uint4 a[NP][2];
 
   template <bool FULL>
-  __device__ __forceinline__ void load(const uint16_t* const (&arow)[kPass][2], int k0, int K) {
+  __device__ __forceinline__ void load(const ARows& rows, int k0, int K) {
     const int k8 = k0 + (threadIdx.x & 7) * 8;
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) a[p][i] = FULL ? ld8h(arow[p][i] + k8) : ld8h_to(arow[p][i] + k8, K - k8);
+      for (int i = 0; i < 2; ++i) {
+        const uint16_t* at = (const uint16_t*)(rows.base[p] + (rows.off[p][i] + (uint32_t)k8 * 2));
+        a[p][i] = FULL ? ld8h(at) : ld8h_to(at, K - k8);
+      }
   }
 
   __device__ __forceinline__ void put(char* lds) const {
@@ -427,7 +437,7 @@ struct ASlab {
 };
 
 template <bool XBF16, int NP>
-__device__ __forceinline__ void slab_product(const XSlab<XBF16>& x, const ASlab<NP>& a, char* lds, v4f (&acc)[kPass]) {
+__device__ __forceinline__ void slab_product(const XSlab<XBF16>& x, const ASlab<NP>& a, char* lds, v4f (&acc)[kMaxPass]) {
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   wave_turn();  // the last slab has been read
   x.put(lds);
@@ -474,17 +484,18 @@ struct Shrink {
 
   // after begin()
   template <int NP>
-  __device__ __forceinline__ void run(const uint16_t* const (&arow)[kPass][2], char* lds, v4f (&acc)[kPass]) {
+  __device__ __forceinline__ void run(const ARows& arow, char* lds, v4f (&acc)[kMaxPass]) {
     if (first < full) {
-      constexpr int D = kAhead + 1, DA = NP <= 2 ? D : 2;  // A comes from the L2: fewer ahead do
+      // A comes from the L2: the more tasks a slab has, the fewer slabs ahead
+      constexpr int D = kAhead + 1, DA = NP <= 2 ? D : NP <= 4 ? 2 : 1;
       ASlab<NP> a[DA];
 #pragma unroll
       for (int i = 0; i < DA - 1; ++i) a[i].template load<true>(arow, slab(i) * 64, K);
       for (int i = 0; first + i * kTileWaves < full; i += D) {
 #pragma unroll
         for (int u = 0; u < D; ++u) {
-          x[(u + D - 1) % D].template load<true>(xrow, slab(i + u + D - 1) * 64, K);
           a[(u + DA - 1) % DA].template load<true>(arow, slab(i + u + DA - 1) * 64, K);
+          x[(u + D - 1) % D].template load<true>(xrow, slab(i + u + D - 1) * 64, K);
           if (first + (i + u) * kTileWaves < full) slab_product<XBF16, NP>(x[u], a[u % DA], lds, acc);
         }
       }
@@ -584,44 +595,48 @@ __device__ __forceinline__ void store_sum(const Four<YBF16> (&y)[4], bool based,
 }
 
 // The second product over whole blocks of 64 outputs, every kTileWaves-th from nb
-// to n1, `steps` steps each, G at a time.  All loads and stores of a block are
+// to n1.  G steps a block (ONCE), their settings in scalar registers throughout;
+// or any number of steps, G at a time.  All loads and stores of a block are
 // unconditional, so the pieces of the next G steps (fetched as soon as the last
 // have gone to LDS) and the next block's base stay in flight meanwhile.
 // `ready` is called once the first loads are under way: v is there after it.
-template <int NS, bool YBF16, int G, class Ready>
-__device__ __forceinline__ void blocks(Ready&& ready, const moe_lora& L, const Step* list, int steps, const int (&slot)[4],
-                                       const size_t (&row)[4], const uint16_t (&vs)[NS][16][kVStride], int nb, int n1,
-                                       const void* base, bool based, void* out, char* lds) {
+template <int NS, bool YBF16, int G, bool ONCE, class Ready>
+__device__ __forceinline__ void blocks(Ready&& ready, const moe_lora& L, const Step* list, int steps,
+                                       const int (&slot)[4], const size_t (&row)[4],
+                                       const uint16_t (&vs)[NS][16][kVStride], int nb, int n1, const void* base,
+                                       bool based, void* out, char* lds) {
   const int n = (threadIdx.x & 15) * 4, r = L.r;
   Four<YBF16> y[4], y_next[4];
   Pieces p[G];
+  Step s[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) s[g] = fetch(list, ONCE ? g : min(g, steps - 1));
   if (nb < n1) {
     load_base(y, base, row, nb + n);
 #pragma unroll
-    for (int g = 0; g < G; ++g) p[g].load(fetch(list, min(g, steps - 1)), nb, r);
+    for (int g = 0; g < G; ++g) p[g].load(s[g], nb, r);
   }
   ready();
   for (; nb < n1; nb += kTileWaves * 64) {
     const int nb2 = nb + kTileWaves * 64 < n1 ? nb + kTileWaves * 64 : nb;
     v4f acc[4] = {}, d[4] = {};
     load_base(y_next, base, row, nb2 + n);
-    for (int u = 0; u < steps; u += G) {
-      const bool end = u + G >= steps;
+    for (int u = 0; u < (ONCE ? G : steps); u += G) {
+      const bool end = ONCE || u + G >= steps;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const Step s = fetch(list, min(u + g, steps - 1));
-        const Step after = fetch(list, end ? min(g, steps - 1) : min(u + G + g, steps - 1));
+        if constexpr (!ONCE) s[g] = fetch(list, min(u + g, steps - 1));
         wave_turn();  // the last pieces have been read
-        p[g].put(s, lds);
+        p[g].put(s[g], lds);
         wave_turn();
-        p[g].load(after, end ? nb2 : nb, r);
-        if (u + g < steps) {  // no memory but LDS in here
-          if (s.j0 == 0) {
+        p[g].load(ONCE ? s[g] : fetch(list, end ? min(g, steps - 1) : min(u + G + g, steps - 1)), end ? nb2 : nb, r);
+        if (ONCE || u + g < steps) {  // no memory but LDS in here
+          if (s[g].j0 == 0) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) d[q] = v4f{0.f, 0.f, 0.f, 0.f};
           }
-          multiply<NS>(s, vs, lds, d);
-          take(s, slot, d, acc);
+          multiply<NS>(s[g], vs, lds, d);
+          take(s[g], slot, d, acc);
         }
       }
     }
@@ -634,8 +649,10 @@ __device__ __forceinline__ void blocks(Ready&& ready, const moe_lora& L, const S
 template <bool XBF16, bool YBF16>
 __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const void* __restrict__ x, int T,
                                                             const int32_t* __restrict__ ids, const void* base,
-                                                            void* out, int per) {
+                                                            void* out, int per, int split, int work) {
   constexpr int NS = YBF16 ? 2 : 3;
+  // tasks per pass over x, and a wavefront's LDS for them: x 2 or 6 KB, A 2 KB a task (later a slab of B)
+  constexpr int kPass = XBF16 ? 8 : 4, kStage = XSlab<XBF16>::kBytes + kPass * 2048;
   __shared__ __align__(16) char stage[kTileWaves][kStage];
   __shared__ __align__(16) uint16_t vs[NS][16][kVStride];
   __shared__ int tok_slot[16], ad_id[16], ad_rank[16], n_task, n_step;
@@ -643,7 +660,11 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
   __shared__ uint8_t task_slot[128], task_tile[128];
   __shared__ Step step[64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
-  const int t0 = blockIdx.x * 16, K = L.K, N = L.N, r = L.r;
+  // workgroups go to the 8 XCDs in turn: each XCD takes a run of tiles, whose
+  // adapters are few and stay in its L2
+  const int each = gridDim.x / 8, w = (blockIdx.x % 8) * each + blockIdx.x / 8;
+  if (w >= work) return;
+  const int t0 = w / split * 16, n0 = w % split * per, K = L.K, N = L.N, r = L.r;
   char* lds = stage[wave];
 
   Shrink<XBF16> ax;
@@ -718,24 +739,26 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
     __syncthreads();
   };
   for (int p0 = 0; p0 < ntask; p0 += kPass) {
-    v4f acc[kPass] = {};
-    const uint16_t* arow[kPass][2];
-#pragma unroll
-    for (int p = 0; p < kPass; ++p)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int q = min(p0 + p, ntask - 1), slot = task_slot[q];
-        const int j = min(task_tile[q] * 16 + i * 8 + (lane >> 3), ad_rank[slot] - 1);
-        arow[p][i] = (const uint16_t*)L.a + ((size_t)ad_id[slot] * r + j) * K;
-      }
+    v4f acc[kMaxPass] = {};
     const int np = min(kPass, ntask - p0);
+    ARows arow;
+#pragma unroll
+    for (int p = 0; p < kPass; ++p) {
+      const int q = min(p0 + p, ntask - 1), slot = __builtin_amdgcn_readfirstlane(task_slot[q]);
+      arow.base[p] = (const char*)L.a + (size_t)__builtin_amdgcn_readfirstlane(ad_id[slot]) * r * K * 2;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        arow.off[p][i] = (uint32_t)min(task_tile[q] * 16 + i * 8 + (lane >> 3), ad_rank[slot] - 1) * (uint32_t)K * 2u;
+    }
     if (p0 > 0) ax.begin();
     if (np == 1)
       ax.template run<1>(arow, lds, acc);
     else if (np == 2)
       ax.template run<2>(arow, lds, acc);
-    else
-      ax.template run<kPass>(arow, lds, acc);
+    else if (np <= 4 || kPass == 4)
+      ax.template run<4>(arow, lds, acc);
+    else if constexpr (kPass == 8)
+      ax.template run<8>(arow, lds, acc);
     wave_turn();
 #pragma unroll
     for (int p = 0; p < kPass; ++p) *(v4f*)(lds + ((p * 16 + col) * 16 + g * 4) * 4) = acc[p];
@@ -752,8 +775,8 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
     slot[i] = tok_slot[g * 4 + i];
     row[i] = (size_t)min(t0 + g * 4 + i, T - 1) * N;
   }
-  const int n1 = min(N, ((int)blockIdx.y + 1) * per);
-  int nb = blockIdx.y * per + wave * 64;
+  const int n1 = min(N, n0 + per);
+  int nb = n0 + wave * 64;
   const bool based = base != nullptr;
   auto last = [&] {
     if (ntask > 0) join((ntask - 1) / kPass * kPass, (ntask - 1) % kPass + 1);
@@ -763,12 +786,21 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
     // last pieces run into the next seven rows, which have to be inside B
     const int whole = r % 8 == 0 ? n1 / 64 * 64 : max(0, min(n1, N - 7)) / 64 * 64;
     const void* from = based ? base : out;
+    auto run = [&](auto g, auto once) {
+      blocks<NS, YBF16, decltype(g)::value, decltype(once)::value>(last, L, step, steps, slot, row, vs, nb, whole, from,
+                                                                   based, out, lds);
+    };
+    using yes = std::true_type;
     if (steps == 1)
-      blocks<NS, YBF16, 1>(last, L, step, steps, slot, row, vs, nb, whole, from, based, out, lds);
+      run(std::integral_constant<int, 1>(), yes());
     else if (steps == 2)
-      blocks<NS, YBF16, 2>(last, L, step, steps, slot, row, vs, nb, whole, from, based, out, lds);
+      run(std::integral_constant<int, 2>(), yes());
+    else if (steps == 3)
+      run(std::integral_constant<int, 3>(), yes());
+    else if (steps == 4)
+      run(std::integral_constant<int, 4>(), yes());
     else
-      blocks<NS, YBF16, 4>(last, L, step, steps, slot, row, vs, nb, whole, from, based, out, lds);
+      run(std::integral_constant<int, 4>(), std::false_type());
     if (nb < whole) nb += (whole - nb + kTileWaves * 64 - 1) / (kTileWaves * 64) * (kTileWaves * 64);
   } else {
     last();
@@ -822,8 +854,9 @@ void run(const moe_lora* L, const void* x, int T, const int32_t* ids, const void
     const int tiles = (T + 15) / 16;
     const int split = max(1, min(kGroups / tiles, (L->N + 63) / 64));  // no second round for a few workgroups
     const int per = ((L->N + split - 1) / split + 63) / 64 * 64;
-    launch(MOE_PROF_LORA, tile_kernel<XBF16, YBF16>, dim3(tiles, (L->N + per - 1) / per), dim3(kTileThreads), 0, s, *L,
-           x, T, ids, base, out, per);
+    const int parts = (L->N + per - 1) / per, work = tiles * parts;
+    launch(MOE_PROF_LORA, tile_kernel<XBF16, YBF16>, dim3((work + 7) / 8 * 8), dim3(kTileThreads), 0, s, *L, x, T, ids,
+           base, out, per, parts, work);
   }
 }
 
