@@ -834,9 +834,9 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
 // (two tokens on one up to rank 16) for a chain of reads; the tile form once a
 // tile and distinct adapter, but takes 8 us for a tile at least.  Both measured
 // over 150 drawn calls (K, N 64..4096, r 1..64, up to 64 requests): this rule is
-// 1.1% off the better of the two on the mean, the token form alone 24%, the tile
-// form alone 97%.  E.g. K = N = 4096, r = 16, bf16: 128 tokens 8.3 against 11.8 us,
-// 1024 tokens 41.6 against 16.2.
+// 1.0% off the better of the two on the mean, the token form alone 23%, the tile
+// form alone 102%.  E.g. K = N = 4096, r = 16, bf16: 128 tokens 8.5 against 11.8 us,
+// 1024 tokens 41.6 against 15.7.
 bool token_form(const moe_lora* L, int T) {
   const double products = (double)T * L->r * ((double)L->K + L->N);
   return T <= 128 || (products <= 24e6 && (T <= 512 || (L->r <= 16 && T <= 1536)));

@@ -4,12 +4,21 @@
 // rounding of it would otherwise change places.
 //
 // One wavefront per token, expert lane + 64 j in register j of a lane.  The k
-// best choices are found without sorting: their 64-bit images (order-preserving
+// best choices are found without sorting: their images (order-preserving
 // integers) are compared with a threshold that is halved in until exactly k are
-// not below it, first on the images' high words, and only where those tie on
-// the low words and then on the expert ids.  A step is one comparison and one
-// count of a lane mask per register, whatever k is.  What is picked goes
-// through LDS in order of expert id and finds its place by counting.
+// not below it.  A step is one comparison and one count of a lane mask per
+// register, whatever k is.
+//
+// An exponential in double precision costs some 70 instructions, and with one
+// for every expert a launch of 4096 tokens is bound by them.  So the choices are
+// first formed in fp32, whose error is bounded, to find which experts can be
+// among the k best at all: those within the bound of the k-th.  They are mostly
+// k, and only they, one a lane, get scores in double precision.  Where fp32
+// cannot tell the groups apart, or leaves more than 64 experts, the wavefront
+// takes every score in double precision instead (as where the bias or an
+// infinity would break the bound, and for softmax with a bias, whose denominator
+// counts in the comparison).
+#include "chunk_dev.h"
 #include "route_dev.h"
 
 namespace moe {
@@ -19,6 +28,12 @@ namespace {
 constexpr int kMaxE = 1024;
 constexpr int kWaves = 4;  // tokens a workgroup
 constexpr uint32_t kMasked = 0x000fffffu;  // high word of -inf's image
+// fp32 choices, with |bias| <= kMaxBias, are off by less than 8e-7: the score by
+// 2.1e-7 (s (1 - s) of the exponential's relative error, |x| 2^-23 and two steps,
+// and the reciprocal's step), the sum with the bias by half a step of 9.  Two of
+// them are told apart beyond twice that; sums of two, rounded once more, beyond
+// 5.4e-6.
+constexpr float kMaxBias = 8.0f, kApart = 2e-6f, kGroupsApart = 8e-6f;
 constexpr float kLowest = -0x1.fep127f;  // bf16's lowest value: a logit there or below masks its expert
 
 __device__ __forceinline__ double make_f64(uint32_t lo, uint32_t hi) {
@@ -88,6 +103,83 @@ __device__ __forceinline__ uint32_t threshold(const uint32_t (&key)[EPL], int ne
   return lo;
 }
 
+__device__ __forceinline__ float readlane_any(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ double readlane_any(double v, int lane) { return readlane_f64(v, lane); }
+
+// what a wavefront's lanes wrote to its LDS may now be read by its other lanes
+__device__ __forceinline__ void wave_turn() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The groups that stay, a bit each, from the choices (-inf: masked).  last: the
+// value of the last that stays; apart: how far it is above the best that does not.
+template <class F, int EPL>
+__device__ __forceinline__ uint64_t best_groups(const moe_router& R, const F (&c)[EPL], F* lds, F* last, F* apart) {
+  const int lane = threadIdx.x & 63, gs = R.E / R.groups;
+  const F inf = (F)INFINITY;
+  int per = 64;  // lanes a group: a power of two
+  while (per * R.groups > 64) per >>= 1;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) lds[lane + 64 * j] = c[j];
+  wave_turn();
+  const int g = lane / per;
+  F first = -inf, second = -inf;  // the two best of this lane's part of its group
+  if (g < R.groups) {
+    for (int i = lane % per; i < gs; i += per) {
+      const F v = lds[g * gs + i];
+      second = fmax(second, fmin(first, v));
+      first = fmax(first, v);
+    }
+  }
+  for (int off = 1; off < per; off *= 2) {
+    const F f = __shfl_xor(first, off, 64), n = __shfl_xor(second, off, 64);
+    second = fmax(fmax(second, n), fmin(first, f));
+    first = fmax(first, f);
+  }
+  const F value = R.group_score == MOE_GROUP_TOP2 && second > -inf ? first + second : first;
+  int rank = 0;
+  for (int i = 0; i < R.groups; ++i) {
+    const F v = readlane_any(value, i * per);
+    rank += v > value || (v == value && i < g);
+  }
+  const bool leads = g < R.groups && lane % per == 0;
+  const uint64_t kept = __ballot(leads && rank < R.topk_groups);
+  *last = readlane_any(value, __ffsll((unsigned long long)__ballot(leads && rank == R.topk_groups - 1)) - 1);
+  *apart = *last - readlane_any(value, __ffsll((unsigned long long)__ballot(leads && rank == R.topk_groups)) - 1);
+  if (per == 1) return kept;
+  uint64_t stay = 0;
+  for (int i = 0; i < R.groups; ++i) stay |= ((kept >> (i * per)) & 1) << i;
+  return stay;
+}
+
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// Lane i < n of the picks' lanes holds one: expert e, score s (ascending e over
+// the lanes).  Writes them in order of falling score, ties to the lower expert.
+__device__ __forceinline__ void write_picks(const moe_router& R, uint64_t picks, int e, double s, double over,
+                                            int32_t* __restrict__ ids, float* __restrict__ w) {
+  const int lane = threadIdx.x & 63;
+  double total = 0.0;
+  int place = 0;
+  for (uint64_t m = picks; m; m &= m - 1) {
+    const int i = __ffsll((unsigned long long)m) - 1;
+    const double v = readlane_f64(s, i);
+    total += v;
+    place += v > s || (v == s && i < lane);
+  }
+  if ((picks >> lane) & 1) {
+    const double by = R.renorm ? total : over;
+    ids[place] = e;
+    w[place] = (float)((by > 0.0 ? s / by : 0.0) * (double)R.scale);
+  }
+}
+
 template <int EPL>
 __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R, int T, uint32_t inv_gs,
                                                                    const void* __restrict__ logits, bool lbf16,
@@ -96,6 +188,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
   __shared__ double choice[kWaves][EPL * 64];
   __shared__ double pick_s[kWaves][64];
   __shared__ int pick_e[kWaves][64];
+  __shared__ float pick_l[kWaves][64], pick_b[kWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = blockIdx.x * kWaves + wave, E = R.E;
   if (t >= T) return;  // the whole wavefront: nothing below is shared between wavefronts
   const double inf = __longlong_as_double(0x7ff0000000000000ll);
@@ -108,16 +201,101 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
     b[j] = bias ? bias[e] : 0.f;
   }
 
-  // scores and choices; a masked expert's are 0 and -inf
-  double s[EPL], c[EPL];
-  if (R.scoring == MOE_SCORE_SIGMOID) {
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) s[j] = l[j] > kLowest ? 1.0 / (1.0 + exp(-(double)l[j])) : 0.0;  // NaN: 0
-  } else {
+  const bool sigmoid_scores = R.scoring == MOE_SCORE_SIGMOID;
+  float top = 0.f;  // softmax: the largest logit
+  if (!sigmoid_scores) {
     uint32_t best = 0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) best = max(best, sel_key(l[j]));
-    const float top = key_value(wave_ext_u32<true>(best));
+    top = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(key_value(wave_ext_u32<true>(best)))));
+  }
+  int32_t* my_ids = ids + (size_t)t * R.k;
+  float* my_w = w + (size_t)t * R.k;
+
+  if (sigmoid_scores || (!bias && top > kLowest && top < INFINITY)) {
+    float c[EPL], sum = 0.f;
+    bool wide = false;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const bool live = l[j] > kLowest;
+      if (sigmoid_scores) {
+        c[j] = sigmoid(l[j]) + b[j];
+        wide |= live && fabsf(b[j]) > kMaxBias;
+        c[j] = live && c[j] == c[j] ? c[j] : -INFINITY;
+      } else {
+        c[j] = __expf(l[j] - top);
+        sum += live && lane + 64 * j < E ? c[j] : 0.f;
+        c[j] = live ? c[j] : -INFINITY;
+      }
+    }
+    bool sure = __ballot(wide) == 0;
+    uint64_t stay = ~0ull;
+    if (sure && R.topk_groups < R.groups) {
+      float last, apart;
+      if (!sigmoid_scores && R.group_score == MOE_GROUP_MAX) {
+        // by the logits themselves, whose ties are ties of the scores; down to where scores underflow
+        float v[EPL];
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) v[j] = l[j] > kLowest ? l[j] : -INFINITY;
+        stay = best_groups<float, EPL>(R, v, (float*)choice[wave], &last, &apart);
+        sure = last > top - 700.f && (apart == 0.f || apart > kApart);
+      } else {
+        stay = best_groups<float, EPL>(R, c, (float*)choice[wave], &last, &apart);
+        sure = apart > kGroupsApart;
+      }
+    }
+    if (sure) {
+      uint32_t key[EPL];
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        const int e = lane + 64 * j;
+        key[j] = e < E && ((stay >> (((uint32_t)e * inv_gs) >> 22)) & 1) ? sel_key(c[j]) : 0u;
+      }
+      constexpr uint32_t kNone = 0x007fffffu;  // -inf's image
+      const uint32_t cut = threshold(key, R.k, kNone);
+      const uint32_t from = cut > kNone ? sel_key(key_value(cut) - kApart) : 0u;
+      const int n = cut > kNone ? count_from(key, from) : 65;
+      if (n <= 64) {  // one candidate a lane, in order of id
+        int at = 0;
+        wave_turn();
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+          const uint64_t in = __ballot(key[j] >= from);
+          if ((in >> lane) & 1) {
+            const int p = at + lanes_below(in);
+            pick_e[wave][p] = lane + 64 * j;
+            pick_l[wave][p] = l[j];
+            pick_b[wave][p] = b[j];
+          }
+          at += __popcll(in);
+        }
+        wave_turn();
+        const int e = pick_e[wave][lane];
+        const double x = (double)pick_l[wave][lane];
+        const double z = exp(sigmoid_scores ? -x : x - (double)top);
+        const double s = sigmoid_scores ? 1.0 / (1.0 + z) : z;
+        uint64_t picks = n == 64 ? ~0ull : (1ull << n) - 1;
+        if (n > R.k) {
+          const double ch = sigmoid_scores ? s + (double)pick_b[wave][lane] : s;
+          int before = 0;
+          for (int i = 0; i < n; ++i) {
+            const double v = readlane_f64(ch, i);
+            before += v > ch || (v == ch && i < lane);
+          }
+          picks = __ballot(lane < n && before < R.k);
+        }
+        write_picks(R, picks, e, s, sigmoid_scores ? 1.0 : (double)wave_sum(sum), my_ids, my_w);
+        return;
+      }
+    }
+  }
+
+  // every score in double precision; a masked expert's are 0 and -inf
+  double s[EPL], c[EPL];
+  if (sigmoid_scores) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) s[j] = l[j] > kLowest ? 1.0 / (1.0 + exp(-(double)l[j])) : 0.0;  // NaN: 0
+  } else {
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
@@ -135,44 +313,11 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
     c[j] = live ? c[j] + 0.0 : -inf;  // -0 becomes 0
     s[j] = live ? s[j] : 0.0;
   }
-
   uint64_t stay = ~0ull;  // groups
   if (R.topk_groups < R.groups) {
-    const int gs = E / R.groups;
-    int per = 64;  // lanes a group: a power of two
-    while (per * R.groups > 64) per >>= 1;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) choice[wave][lane + 64 * j] = c[j];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    const int g = lane / per;
-    double first = -inf, second = -inf;  // the two best of this lane's part of its group
-    if (g < R.groups) {
-      for (int i = lane % per; i < gs; i += per) {
-        const double v = choice[wave][g * gs + i];
-        second = fmax(second, fmin(first, v));
-        first = fmax(first, v);
-      }
-    }
-    for (int off = 1; off < per; off *= 2) {
-      const double f = __shfl_xor(first, off, 64), n = __shfl_xor(second, off, 64);
-      second = fmax(fmax(second, n), fmin(first, f));
-      first = fmax(first, f);
-    }
-    const double value = R.group_score == MOE_GROUP_TOP2 && second > -inf ? first + second : first;
-    int rank = 0;
-    for (int i = 0; i < R.groups; ++i) {
-      const double v = readlane_f64(value, i * per);
-      rank += v > value || (v == value && i < g);
-    }
-    const uint64_t kept = __ballot(g < R.groups && rank < R.topk_groups && lane % per == 0);
-    if (per == 1) {
-      stay = kept;
-    } else {
-      stay = 0;
-      for (int i = 0; i < R.groups; ++i) stay |= ((kept >> (i * per)) & 1) << i;
-    }
+    double last, apart;
+    wave_turn();
+    stay = best_groups<double, EPL>(R, c, choice[wave], &last, &apart);
   }
 
   // images: 0 for what is no candidate
@@ -227,42 +372,26 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {  // equal choices: the lower ids
       const uint64_t same = __ballot(bit[j] == cut2);
-      const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
+      const int before = lanes_below(same);
       take[j] |= __ballot(bit[j] == cut2 && before < left);
       left -= min(left, (int)__popcll(same));
     }
   }
 
-  // picks in order of id, then each to its place: falling score, ties to the lower id
+  // picks to the lanes in order of id
   int from = 0;
+  wave_turn();
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     if ((take[j] >> lane) & 1) {
-      const int p = from + __builtin_amdgcn_mbcnt_hi((uint32_t)(take[j] >> 32),
-                                                     __builtin_amdgcn_mbcnt_lo((uint32_t)take[j], 0));
+      const int p = from + lanes_below(take[j]);
       pick_s[wave][p] = s[j];
       pick_e[wave][p] = lane + 64 * j;
     }
     from += __popcll(take[j]);
   }
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  const double mine = pick_s[wave][lane];
-  const int e = pick_e[wave][lane];
-  double total = 0.0;
-  int place = 0;
-  for (int i = 0; i < R.k; ++i) {
-    const double v = readlane_f64(mine, i);
-    total += v;
-    place += v > mine || (v == mine && i < lane);
-  }
-  if (lane < R.k) {
-    double v = mine;
-    if (R.renorm) v = total > 0.0 ? v / total : 0.0;
-    ids[(size_t)t * R.k + place] = e;
-    w[(size_t)t * R.k + place] = (float)(v * (double)R.scale);
-  }
+  wave_turn();
+  write_picks(R, R.k == 64 ? ~0ull : (1ull << R.k) - 1, pick_e[wave][lane], pick_s[wave][lane], 1.0, my_ids, my_w);
 }
 
 }  // namespace

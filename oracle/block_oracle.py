@@ -7,8 +7,6 @@ shared with the library.  Each function is pinned by a closed form or a brute
 force in tests/test_oracle_block.py."""
 from __future__ import annotations
 
-import math
-
 import numpy as np
 
 
@@ -52,7 +50,8 @@ def route_groups(logits, k, scoring="sigmoid", bias=None, groups=1, topk_groups=
     for t in range(T):
         l = [float(v) if v > -(2.0 - 2.0 ** -7) * 2.0 ** 127 else -np.inf for v in logits[t]]
         if scoring == "sigmoid":
-            s = [0.0 if v == -np.inf else 1.0 / (1.0 + math.exp(-v)) if v > -709.0 else 0.0 for v in l]
+            with np.errstate(over="ignore"):  # an exponential past the range: a score of 0
+                s = [0.0 if v == -np.inf else float(1.0 / (1.0 + np.exp(-v))) for v in l]
         else:
             top = max(l)
             e = [0.0 if v == -np.inf else 1.0 if v == top else np.exp(v - top) for v in l]

@@ -245,8 +245,9 @@ def _route(gpu_lib, logits, k, bias=None, lt="f32", shift=0, **kw):
     rid, rw = B.route_groups(_f64(lg), k, bias=None if b is None else _f64(b), **kw)
     got_i, got_w = ids.check().cpu().numpy(), _f64(w.check())
     assert np.array_equal(got_i, rid), (kw, np.argwhere(got_i != rid)[:4])
-    # scores and their sum in at most 16 roundings of 2^-24
-    _close(got_w, rw, np.abs(rw) * 16 * U, f"weights {kw}")
+    # scores and their sum in at most 16 roundings of 2^-24; the last one, to fp32, is
+    # off by half of 2^-149 below 2^-126, where fp32's steps stop shrinking
+    _close(got_w, rw, np.abs(rw) * 16 * U + 2.0 ** -150, f"weights {kw}")
     return got_i, got_w
 
 
@@ -329,6 +330,30 @@ def test_route_groups_choices_closer_than_fp32(gpu_lib):
             _route(gpu_lib, lg, 8, b, **kw)
     one = np.float32(1 / (1 + np.exp(-lg.astype(np.float64)[3])))
     _route(gpu_lib, np.repeat(lg[3:], 2, 0), 8, -one)
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E", [48, 256, 640])
+def test_route_groups_crowds(gpu_lib, E, scoring):
+    """Choices crowded into a few fp32 steps, so that fp32 scores tell neither the
+    experts nor the groups apart; some rows with only a few in the crowd; biases at
+    and beyond 8, where fp32 sums lose the score's bits; logits thousands apart,
+    whose softmax underflows even in double precision."""
+    rng = np.random.default_rng(E)
+    T, k = 40, 7
+    step = np.float32(2.0 ** -22)
+    tight = np.float32(2.0) + rng.integers(0, 9, (T, E)).astype(np.float32) * step
+    mixed = np.where(rng.random((T, E)) < 12 / E, tight, -1.0 - rng.random((T, E)).astype(np.float32))
+    far = -2000.0 * rng.random((T, E)).astype(np.float32)
+    plain = rng.standard_normal((T, E)).astype(np.float32)
+    small = rng.integers(0, 5, E).astype(np.float32) * step
+    wide = np.where(rng.random(E) < 0.3, rng.choice([8.0, -8.0, 7.9, 8.1, 1e4, -1e30], E), 0.1 * rng.standard_normal(E))
+    wide = (wide + small).astype(np.float32)
+    for kw in (dict(), dict(groups=8, topk_groups=3), dict(groups=16, topk_groups=9)):
+        for gscore in ("max", "top2"):
+            for lg in (tight, mixed, far, plain):
+                for bias in (None, small, wide):
+                    _route(gpu_lib, lg, k, bias, scoring=scoring, group_score=gscore, renorm=lg is not plain, **kw)
 
 
 def test_route_groups_matches_moe_route(gpu_lib):
