@@ -1,6 +1,7 @@
 // Chunks of eight consecutive bf16 or fp32 elements at any element-aligned
 // address: one or two 16-byte accesses where all eight are there (the hardware
 // takes global accesses at any alignment), single elements at the end of a row.
+// Shared by the norms, the adapters and the routing by groups.
 #pragma once
 
 #include "common.h"
@@ -142,5 +143,12 @@ __device__ __forceinline__ float load1(const void* p, bool bf16, size_t at) {
 // 1 / (1 + e^-g): the hardware's exponential of 2 and reciprocal, each within a
 // step of fp32, the argument's rounding growing with |g|
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+// what a wavefront's lanes wrote to its LDS may now be read by its other lanes
+__device__ __forceinline__ void wave_turn() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 }  // namespace moe

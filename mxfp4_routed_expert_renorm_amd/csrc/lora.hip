@@ -2,12 +2,12 @@
 // (moe_lora_add): out[t] = base[t] + scale * B (A x[t]) with the adapter of
 // the token's request.
 //
-// Two forms, chosen by the number of tokens:
+// Two forms, chosen by the host from the sizes (token_form):
 //   - token_kernel: one token a workgroup on the vector units, so a decode
 //     batch whose tokens all have adapters of their own reads each adapter
 //     once;
-//   - tile_kernel: 16 tokens a workgroup on the matrix units, one pass per
-//     distinct adapter of the 16.
+//   - tile_kernel: 16 tokens a workgroup on the matrix units, a product for
+//     every distinct adapter of the 16.
 // Both compute A x whole in every workgroup that needs it (from the caches
 // after the first) and split the outputs over workgroups, so the call is one
 // launch and needs no workspace.
@@ -35,7 +35,10 @@ __device__ __forceinline__ int rank_of(const moe_lora& L, int id) {
 // each with its eight ranks of v in registers, so that a wavefront's loads are
 // contiguous.  The first rows of B and the base do not depend on A x and are
 // requested before it: what is left is a chain of the id, the adapter's rank, A
-// and the reductions.
+// and the reductions.  That chain bounds small calls (K = N = 4096, rank 16, one
+// token: 4.3 us, of which 1.9 are a launch); larger ranks are bound by what one
+// compute unit draws (rank 64, 64 tokens of 64 adapters: 16.8 us, 67 MB, 4.0 TB/s;
+// with ranks 8 to 64 mixed the tokens of rank 64 set the pace: 17.3 us).
 
 constexpr int kTokThreads = 512, kTokWaves = kTokThreads / 64;
 constexpr int kTokOut = 1024;  // outputs gathered in LDS before they are written
@@ -123,7 +126,7 @@ template <bool XBF16, bool YBF16, int LANES, int R, int S>
 __device__ __forceinline__ void token_body(const moe_lora& L, const void* __restrict__ x, int t, int rank, float scale,
                                            const uint16_t* __restrict__ A, const uint16_t* __restrict__ B,
                                            const void* base, void* out, int n0, int n1, float* v, float* o) {
-  constexpr int kRows = 64 / LANES, kStep = kTokWaves * kRows;    // rows of B a wavefront, a workgroup loads at once
+  constexpr int kRows = 64 / LANES, kStep = kTokWaves * kRows;   // rows of B a wavefront, a workgroup loads at once
   constexpr int U = kStep * 8 <= kTokOut ? 8 : kTokOut / kStep;  // such loads in flight
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = L.r, part = (lane % LANES) * 8;
   const size_t yt = (size_t)t * L.N, end = (size_t)L.N * r;  // end of B
@@ -189,11 +192,13 @@ __device__ __forceinline__ void token_body(const moe_lora& L, const void* __rest
   }
 }
 
-// WIDE: banks of ranks over 16
+// WIDE: banks of ranks over 16, whose forms take so many registers that a compute
+// unit holds one workgroup instead of two: without the split, 400 tokens of
+// K = N = 1024, rank 4, take 5.3 us instead of 3.9.
 template <bool XBF16, bool YBF16, bool WIDE>
 __global__ __launch_bounds__(kTokThreads, WIDE ? 2 : 4) void token_kernel(moe_lora L, const void* __restrict__ x,
-                                                            const int32_t* __restrict__ ids, const void* base,
-                                                            void* out, int per) {
+                                                                          const int32_t* __restrict__ ids,
+                                                                          const void* base, void* out, int per) {
   __shared__ __align__(16) float v[kMaxRank];
   __shared__ __align__(16) float o[kTokOut];
   constexpr int S = XBF16 ? 8 : 4;
@@ -247,10 +252,14 @@ __global__ __launch_bounds__(kTokThreads, WIDE ? 2 : 4) void token_kernel(moe_lo
 //
 // B v: first operand the tokens' parts, second 16 outputs.  Column m of product q
 // stands for output 4 m + q of a block of 64, so that four products leave four
-// consecutive outputs of four tokens in each lane, a line of each token in 16.  B comes in slabs of up
-// to four chunks of eight ranks; the parts of v over them fill a product's four
-// chunks.  Each adapter's product goes to its own tokens only, so one adapter's
-// NaN cannot reach another's tokens.
+// consecutive outputs of four tokens in each lane, a line of each token in 16.  B
+// comes in slabs of 32 ranks.  Each adapter's product goes to its own tokens only,
+// so one adapter's NaN cannot reach another's tokens.
+//
+// Large calls are bound by memory: 4096 tokens, K = N = 4096, rank 32, bf16, one
+// request: 24.0 us, 4.2 TB/s over x, base, out and the adapter (5.1 is a copy's
+// rate).  A tile at the border of two requests takes longer than the others, and
+// at 4096 tokens every compute unit has one tile: twelve requests 30.3 us.
 
 constexpr int kTileWaves = 8, kTileThreads = 64 * kTileWaves;
 constexpr int kMaxPass = 8;             // most tasks per pass over x
@@ -262,13 +271,6 @@ __device__ __forceinline__ uint16_t take_bf16(float& f) {
   const float rest = f - __uint_as_float(u);
   f = rest == rest ? rest : 0.0f;  // an infinity leaves nothing over
   return (uint16_t)(u >> 16);
-}
-
-// what a wavefront's lanes wrote to its LDS may now be read by its other lanes
-__device__ __forceinline__ void wave_turn() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // four consecutive outputs of a token, n of them (<= 0: none) inside N
@@ -354,7 +356,7 @@ struct Four {
 // and load.  FULL: the slab lies inside K.
 template <bool XBF16>
 struct XSlab {
-  static constexpr int kX = XBF16 ? 2 : 4;                                    // pieces a lane
+  static constexpr int kX = XBF16 ? 2 : 4;                                  // pieces a lane
   static constexpr int kParts = XBF16 ? 1 : 3, kBytes = kParts * 16 * 128;  // bf16 parts of an element in LDS
   uint4 x[kX];
 

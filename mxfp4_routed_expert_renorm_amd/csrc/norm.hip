@@ -8,6 +8,14 @@
 // their registers from its only read to its writes, so out may overwrite an
 // input.  A thread holds V chunks of eight consecutive elements; everything a
 // row needs (weights and gate too) is requested before the first sum is formed.
+// Sums and everything between are fp32; each output is rounded once.
+//
+// Bound by memory: 4096 x 4096 bf16, norm_in 13.3 us (67 MB, 5.0 TB/s; a copy
+// reaches 5.1), norm_out with a channel gate and the next norm 29.0 us (134 MB,
+// 4.6 TB/s).  Large results are stored streaming: with ordinary stores the lines
+// left dirty in the L2s are written back at the kernel's end, 15.0 and 36.0 us.
+// Rows of odd width pay for stores that share lines: 509 x 2047 7.1 us, 509 x 2048
+// 5.4.  One row: 2.4 and 3.5 us, of which 1.9 are a launch.
 #include "chunk_dev.h"
 
 namespace moe {
@@ -140,11 +148,14 @@ struct Shape {
   int v;
 };
 
-// Two chunks a thread where there are rows enough to fill the card, one where a
-// row's latency is what counts.
+// One chunk a thread up to 2^21 elements, where a row's latency counts, two (and
+// streaming stores) above, where bandwidth does.  norm_in at H = 4096 with one and
+// two: 1 row 2.5 and 2.9 us, 256 rows 3.0 and 3.3, 512 rows 3.5 and 3.5, 1024 rows
+// 5.2 and 4.1, 4096 rows 15.2 and 13.0; 1024 x 2048 3.5 and 3.6; norm_out at
+// H = 4096: 1 row 3.6 and 4.8, 512 rows 5.9 and 5.8, 4096 rows 34.2 and 28.7.
 Shape shape(NormArgs& a) {
   const int chunks = (a.H + 7) / 8;
-  const int v = chunks > 1024 || a.T > 256 ? 2 : 1;
+  const int v = chunks > 1024 || (size_t)a.T * a.H > (size_t)1 << 21 ? 2 : 1;
   int per = 64;
   while (per * v < chunks) per *= 2;
   const int block = max(per, 256), rows = block / per;

@@ -18,6 +18,12 @@
 // takes every score in double precision instead (as where the bias or an
 // infinity would break the bound, and for softmax with a bias, whose denominator
 // counts in the comparison).
+//
+// Instructions and their latency bound it, not bytes: 4096 tokens of 256 experts
+// (sigmoid, bias, 8 of 256 out of 4 of 8 groups) 10.1 us, 447 vector and 470
+// scalar instructions a wavefront, four wavefronts a SIMD; with every score in
+// double 10.9 us, with k rounds of a maximum over 64-bit values 36 us.  One
+// token: 5.4 us.
 #include "chunk_dev.h"
 #include "route_dev.h"
 
@@ -107,13 +113,6 @@ __device__ __forceinline__ float readlane_any(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
 __device__ __forceinline__ double readlane_any(double v, int lane) { return readlane_f64(v, lane); }
-
-// what a wavefront's lanes wrote to its LDS may now be read by its other lanes
-__device__ __forceinline__ void wave_turn() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
 
 // The groups that stay, a bit each, from the choices (-inf: masked).  last: the
 // value of the last that stays; apart: how far it is above the best that does not.

@@ -484,6 +484,71 @@ def test_lora_empty_bank_and_no_tokens(gpu_lib):
     torch.cuda.synchronize()
 
 
+# ------------------------------------------------ offsets past 32 bits of elements
+
+def test_far_rows_of_large_calls(gpu_lib):
+    """Rows whose element offsets pass 2^31: the bits of a call on those rows alone."""
+    torch = _torch()
+    rows, H = 2000, 4096
+    T = 300 * rows                                       # 2.46e9 elements
+    some = torch.randn(rows, H, device="cuda").bfloat16()
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    x.view(-1, rows, H).copy_(some)
+    x[-rows:] = some.flip(0)
+    tail = x[-rows:].clone()
+    out, want = torch.empty_like(x), torch.empty_like(tail)
+    norm = gpu_lib.make_norm(H, post=torch.ones(H, device="cuda"))
+    gpu_lib.moe_norm_in(norm, x, out)
+    gpu_lib.moe_norm_in(norm, tail, want)
+    torch.cuda.synchronize()
+    assert torch.equal(out[-rows:], want)
+    gpu_lib.moe_norm_out(norm, x, x, None, out)
+    gpu_lib.moe_norm_out(norm, tail, tail, None, want)
+    torch.cuda.synchronize()
+    assert torch.equal(out[-rows:], want)
+    a = torch.randn(3, 16, H, device="cuda").bfloat16()
+    b = torch.randn(3, H, 16, device="cuda").bfloat16()
+    ids = (torch.arange(T, device="cuda") // 500 % 4).int()
+    lora = gpu_lib.make_lora(a, b)
+    gpu_lib.moe_lora_add(lora, x, ids, x, out)
+    gpu_lib.moe_lora_add(lora, tail, ids[-rows:].clone(), tail, want)
+    torch.cuda.synchronize()
+    assert torch.equal(out[-rows:], want)
+    del x, out
+    T, E, k = 1 << 20, 1024, 8
+    lg = torch.empty(T, E, device="cuda")                # 1.07e9 elements, 4.3e9 bytes
+    one = torch.randn(4096, E, device="cuda")
+    lg.view(-1, 4096, E).copy_(one)
+    lg[-4096:] = one.flip(0)
+    i0, w0 = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    i1, w1 = torch.empty(4096, k, dtype=torch.int32, device="cuda"), torch.empty(4096, k, device="cuda")
+    router = gpu_lib.make_router(E, k, groups=8, topk_groups=3)
+    gpu_lib.moe_route_groups(router, lg, None, i0, w0)
+    gpu_lib.moe_route_groups(router, lg[-4096:].clone(), None, i1, w1)
+    torch.cuda.synchronize()
+    assert torch.equal(i0[-4096:], i1) and torch.equal(w0[-4096:], w1)
+
+
+@pytest.mark.parametrize("T", [7, 2000])
+def test_lora_far_adapters(gpu_lib, T):
+    """The last adapters of a bank of 2.6e9 elements: the bits of a bank of them alone."""
+    torch = _torch()
+    num, r, K, N = 5000, 128, 4096, 4096
+    small_a = torch.randn(2, r, K, device="cuda").bfloat16()
+    small_b = torch.randn(2, N, r, device="cuda").bfloat16()
+    a, b = torch.zeros(num, r, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(num, N, r, dtype=torch.bfloat16,
+                                                                                    device="cuda")
+    a[-2:], b[-2:] = small_a, small_b
+    x = torch.randn(T, K, device="cuda").bfloat16()
+    ids = (torch.arange(T, device="cuda") * 2 // T).int()
+    base = torch.randn(T, N, device="cuda").bfloat16()
+    out, want = torch.empty_like(base), torch.empty_like(base)
+    gpu_lib.moe_lora_add(gpu_lib.make_lora(a, b), x, ids + (num - 2), base, out)
+    gpu_lib.moe_lora_add(gpu_lib.make_lora(small_a, small_b), x, ids, base, want)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
 # ------------------------------------------------------------- the run of them
 
 def _block(gpu_lib, T, E, H, I, k, seed, prefill):
