@@ -76,6 +76,7 @@ class moe_router(ctypes.Structure):
 
 
 class moe_norm(ctypes.Structure):
+    _dev, _tensors = None, ()  # device of the tensors it keeps, and these
     _fields_ = [
         ("H", c_int), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("wt", c_int),
         ("pre_w", c_void_p), ("post_w", c_void_p), ("post_norm", c_int), ("gate", c_int), ("gate_act", c_int),
@@ -84,6 +85,7 @@ class moe_norm(ctypes.Structure):
 
 
 class moe_lora(ctypes.Structure):
+    _dev, _tensors = None, ()  # device of the tensors it keeps, and these
     _fields_ = [
         ("K", c_int), ("N", c_int), ("r", c_int), ("num", c_int),
         ("a", c_void_p), ("b", c_void_p), ("scale", c_void_p), ("ranks", c_void_p),
@@ -260,61 +262,48 @@ def moe_group_wide(keys, nkeys, counts, offsets, perm, scratch, stream=None):
 #
 # These calls take a descriptor made once (make_router, make_norm, make_lora) and
 # tensors that are checked on every call: shape, type, density and one device,
-# which must be the current one.
+# which must be the current one.  Next to a launch a check costs as much as the
+# call itself, so a call tests its tensors in one expression and leaves it to
+# _refuse to say what is wrong.
 
-def _ptr(name, what, t, shape, dtypes, dev):
-    """The address of a dense GPU tensor of this shape and one of these types."""
-    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
-        return t.data_ptr()
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: {what} is {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: {what} must be dense (row-major, contiguous)")
-    raise ValueError(f"{name}: {what} is on {t.device}, not on cuda:{dev}")
-
-
-def _current(name, t):
-    """Device index of a call's first tensor, which must be the current device."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name}: tensors must be on the GPU")
-    now = _torch()._C._cuda_getDevice()
-    if dev != now:
-        raise ValueError(f"{name}: the tensors are on cuda:{dev}, the current device is cuda:{now}")
-    return dev
-
-
-_torch_module = None
-
-
-def _torch():
-    global _torch_module
-    if _torch_module is None:
-        import torch
-        _torch_module = torch
-    return _torch_module
-
-
-_type_codes = None
+_torch_module = _type_codes = _device_now = _stream_now = None
 
 
 def _types():
     """Element types of activations and their codes."""
-    global _type_codes
+    global _torch_module, _type_codes, _device_now, _stream_now
     if _type_codes is None:
-        torch = _torch()
+        import torch
+        _torch_module = torch
+        _device_now, _stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         _type_codes = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
     return _type_codes
 
 
-def _stream_of(stream, dev):
-    """The given stream, or the current one of the device (the raw handle: making
-    a stream object costs as much as a launch)."""
-    if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(dev)
-    return _stream(stream)
+def _refuse(name, descriptors, tensors):
+    """Raises for the first of a call's (what, tensor, shape, types) that is not a
+    dense tensor of this shape and one of these types on the current device."""
+    _, first, _, _ = tensors[0]
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: tensors must be on the GPU")
+    if dev != _device_now():
+        raise ValueError(f"{name}: the tensors are on cuda:{dev}, the current device is cuda:{_device_now()}")
+    for d in descriptors:
+        if d._dev is not None and d._dev != dev:
+            raise ValueError(f"{name}: the descriptor's tensors are on device {d._dev}, the call's on cuda:{dev}")
+    for what, t, shape, dtypes in tensors:
+        if t is None:
+            continue
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: {what} is {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: {what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: {what} must be dense (row-major, contiguous)")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: {what} is on {t.device}, not on cuda:{dev}")
+    raise ValueError(f"{name}: arguments refused")
 
 
 def _plan_tensor(name, what, t, shape, dtype):
@@ -337,11 +326,6 @@ def _one_device(name, tensors):
     return devs.pop() if devs else None
 
 
-def _same_device(name, desc, dev):
-    if desc._dev is not None and desc._dev != dev:
-        raise ValueError(f"{name}: the descriptor's tensors are on device {desc._dev}, the call's on cuda:{dev}")
-
-
 def make_router(E, k, scoring="sigmoid", groups=1, topk_groups=None, group_score="top2", renorm=True,
                 scale=1.0) -> moe_router:
     """Settings of moe_route_groups; topk_groups None: every group stays."""
@@ -352,15 +336,23 @@ def make_router(E, k, scoring="sigmoid", groups=1, topk_groups=None, group_score
 
 def moe_route_groups(router: moe_router, logits, bias, ids, w, stream=None):
     """logits [T, E] (float32 or bfloat16), bias [E] float32 or None -> ids [T, k] int32, w [T, k] float32."""
-    torch, name, types = _torch(), "moe_route_groups", _types()
-    dev = _current(name, logits)
-    T, E, k = logits.shape[0], router.E, router.k
-    st = load().moe_route_groups(
-        ctypes.byref(router), _ptr(name, "logits", logits, (T, E), types, dev), types[logits.dtype],
-        None if bias is None else _ptr(name, "bias", bias, (E,), (torch.float32,), dev), T,
-        _ptr(name, "ids", ids, (T, k), (torch.int32,), dev), _ptr(name, "w", w, (T, k), (torch.float32,), dev),
-        _stream_of(stream, dev))
-    _check(name, st)
+    types, shape, dev = _type_codes or _types(), logits.shape, logits.get_device()
+    T, E, k, torch = shape[0], router.E, router.k, _torch_module
+    code = types.get(logits.dtype)
+    picks = ids.shape
+    if not (code is not None and shape == (T, E) and picks == (T, k) and picks == w.shape
+            and ids.dtype is torch.int32 and w.dtype is torch.float32
+            and dev >= 0 and dev == _device_now() and dev == ids.get_device() and dev == w.get_device()
+            and logits.is_contiguous() and ids.is_contiguous() and w.is_contiguous()
+            and (bias is None or (bias.dtype is torch.float32 and bias.shape == (E,) and bias.is_contiguous()
+                                  and dev == bias.get_device()))):
+        _refuse("moe_route_groups", (), (("logits", logits, (T, E), types), ("bias", bias, (E,), (torch.float32,)),
+                                         ("ids", ids, (T, k), (torch.int32,)), ("w", w, (T, k), (torch.float32,))))
+    st = load().moe_route_groups(ctypes.addressof(router), logits.data_ptr(), code,
+                                 None if bias is None else bias.data_ptr(), T, ids.data_ptr(), w.data_ptr(),
+                                 _stream_now(dev) if stream is None else _stream(stream))
+    if st:
+        _check("moe_route_groups", st)
     return ids, w
 
 
@@ -387,13 +379,18 @@ def make_norm(H, eps=1e-6, pre=None, post=None, post_norm=None, weight_offset=0.
 
 def moe_norm_in(norm: moe_norm, x, out, stream=None):
     """out [T, H] = RMS(x [T, H]; pre)."""
-    name, types = "moe_norm_in", _types()
-    dev = _current(name, x)
-    _same_device(name, norm, dev)
-    shape = (x.shape[0], norm.H)
-    st = load().moe_norm_in(ctypes.byref(norm), _ptr(name, "x", x, shape, types, dev), types[x.dtype], shape[0],
-                            _ptr(name, "out", out, shape, types, dev), types[out.dtype], _stream_of(stream, dev))
-    _check(name, st)
+    types, shape, dev = _type_codes or _types(), x.shape, x.get_device()
+    xt, ot = types.get(x.dtype), types.get(out.dtype)
+    if not (xt is not None and ot is not None and shape == (shape[0], norm.H) and shape == out.shape
+            and dev >= 0 and dev == _device_now() and dev == out.get_device()
+            and (norm._dev is None or norm._dev == dev)
+            and x.is_contiguous() and out.is_contiguous()):
+        want = (shape[0], norm.H)
+        _refuse("moe_norm_in", (norm,), (("x", x, want, types), ("out", out, want, types)))
+    st = load().moe_norm_in(ctypes.addressof(norm), x.data_ptr(), xt, shape[0], out.data_ptr(), ot,
+                            _stream_now(dev) if stream is None else _stream(stream))
+    if st:
+        _check("moe_norm_in", st)
     return out
 
 
@@ -401,31 +398,40 @@ def moe_norm_out(norm: moe_norm, y, residual, gate, out, next=None, next_out=Non
     """out [T, H] = residual + alpha * act(gate) * RMS(y; post) and, with next_out
     [T, H], next_out = RMS(out before its rounding; next's pre).  gate: None, [H],
     [T] or [T, H], as the norm says.  Without next_out, next is not used."""
-    name, types = "moe_norm_out", _types()
-    dev = _current(name, y)
-    _same_device(name, norm, dev)
-    T, H = y.shape[0], norm.H
-    shape = (T, H)
-    if residual.dtype != out.dtype:
-        raise TypeError(f"{name}: residual is {residual.dtype}, out is {out.dtype}")
+    types, shape, dev = _type_codes or _types(), y.shape, y.get_device()
+    T, H, kind = shape[0], norm.H, norm.gate
+    yt, rt = types.get(y.dtype), types.get(out.dtype)
+    good = (yt is not None and rt is not None and residual.dtype is out.dtype
+            and shape == (T, H) and shape == residual.shape and shape == out.shape
+            and dev >= 0 and dev == _device_now() and dev == residual.get_device() and dev == out.get_device()
+            and (norm._dev is None or norm._dev == dev)
+            and y.is_contiguous() and residual.is_contiguous() and out.is_contiguous())
     gp = gt = np_ = nt = nd = None
-    if norm.gate != GATE_NONE and gate is None:
-        raise ValueError(f"{name}: the norm has a gate, the call has none")
+    if (gate is None) != (kind == GATE_NONE):
+        raise ValueError("moe_norm_out: " + ("the norm has no gate" if kind == GATE_NONE
+                                             else "the norm has a gate, the call has none"))
     if gate is not None:
-        if norm.gate == GATE_NONE:
-            raise ValueError(f"{name}: the norm has no gate")
-        gp = _ptr(name, "gate", gate, ((H,), (T,), shape)[norm.gate - 1], types, dev)
-        gt = types[gate.dtype]
+        gt, gp = types.get(gate.dtype), gate.data_ptr()
+        good = (good and gt is not None and gate.shape == ((H,) if kind == GATE_CHANNEL else (T,) if kind == GATE_TOKEN
+                                                           else shape)
+                and gate.is_contiguous() and dev == gate.get_device())
     if next_out is not None:
         if next is None:
-            raise ValueError(f"{name}: next_out needs the next block's norm")
-        _same_device(name, next, dev)
-        np_, nt, nd = _ptr(name, "next_out", next_out, shape, types, dev), types[next_out.dtype], ctypes.byref(next)
-    st = load().moe_norm_out(
-        ctypes.byref(norm), _ptr(name, "y", y, shape, types, dev), types[y.dtype],
-        _ptr(name, "residual", residual, shape, types, dev), gp, gt or 0, T, _ptr(name, "out", out, shape, types, dev),
-        types[out.dtype], nd, np_, nt or 0, _stream_of(stream, dev))
-    _check(name, st)
+            raise ValueError("moe_norm_out: next_out needs the next block's norm")
+        nt, np_, nd = types.get(next_out.dtype), next_out.data_ptr(), ctypes.addressof(next)
+        good = (good and nt is not None and shape == next_out.shape and next_out.is_contiguous()
+                and dev == next_out.get_device() and (next._dev is None or next._dev == dev))
+    if not good:
+        want = (T, H)
+        _refuse("moe_norm_out", (norm,) if next_out is None else (norm, next),
+                (("y", y, want, types), ("residual", residual, want, types), ("out", out, want, (residual.dtype,)),
+                 ("gate", gate, ((H,) if kind == GATE_CHANNEL else (T,) if kind == GATE_TOKEN else want), types),
+                 ("next_out", next_out, want, types)))
+    st = load().moe_norm_out(ctypes.addressof(norm), y.data_ptr(), yt, residual.data_ptr(), gp, gt or 0, T,
+                             out.data_ptr(), rt, nd, np_, nt or 0,
+                             _stream_now(dev) if stream is None else _stream(stream))
+    if st:
+        _check("moe_norm_out", st)
     return out
 
 
@@ -449,18 +455,24 @@ def make_lora(a, b, scale=None, ranks=None) -> moe_lora:
 def moe_lora_add(lora: moe_lora, x, adapter_ids, base, out, stream=None):
     """out [T, N] = base [T, N] (or zeros) + scale * B (A x [T, K]) with each token's
     adapter, adapter_ids [T] int32 (outside the bank: none)."""
-    torch, name, types = _torch(), "moe_lora_add", _types()
-    dev = _current(name, x)
-    _same_device(name, lora, dev)
-    T = x.shape[0]
-    if base is not None and base.dtype != out.dtype:
-        raise TypeError(f"{name}: base is {base.dtype}, out is {out.dtype}")
-    st = load().moe_lora_add(
-        ctypes.byref(lora), _ptr(name, "x", x, (T, lora.K), types, dev), types[x.dtype], T,
-        _ptr(name, "adapter_ids", adapter_ids, (T,), (torch.int32,), dev),
-        None if base is None else _ptr(name, "base", base, (T, lora.N), types, dev),
-        _ptr(name, "out", out, (T, lora.N), types, dev), types[out.dtype], _stream_of(stream, dev))
-    _check(name, st)
+    types, shape, dev = _type_codes or _types(), x.shape, x.get_device()
+    T, K, N, outs = shape[0], lora.K, lora.N, out.shape
+    xt, yt = types.get(x.dtype), types.get(out.dtype)
+    if not (xt is not None and yt is not None and adapter_ids.dtype is _torch_module.int32
+            and shape == (T, K) and outs == (T, N) and adapter_ids.shape == (T,)
+            and dev >= 0 and dev == _device_now() and dev == adapter_ids.get_device() and dev == out.get_device()
+            and (lora._dev is None or lora._dev == dev)
+            and x.is_contiguous() and adapter_ids.is_contiguous() and out.is_contiguous()
+            and (base is None or base is out or (base.dtype is out.dtype and base.shape == outs and base.is_contiguous()
+                                                 and dev == base.get_device()))):
+        _refuse("moe_lora_add", (lora,),
+                (("x", x, (T, K), types), ("adapter_ids", adapter_ids, (T,), (_torch_module.int32,)),
+                 ("out", out, (T, N), types), ("base", base, (T, N), (out.dtype,))))
+    st = load().moe_lora_add(ctypes.addressof(lora), x.data_ptr(), xt, T, adapter_ids.data_ptr(),
+                             None if base is None else base.data_ptr(), out.data_ptr(), yt,
+                             _stream_now(dev) if stream is None else _stream(stream))
+    if st:
+        _check("moe_lora_add", st)
     return out
 
 

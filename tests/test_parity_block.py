@@ -728,3 +728,40 @@ def test_binding_refuses_bad_tensors(gpu_lib):
     with pytest.raises(gpu_lib.MoeError, match="next_out"):
         gpu_lib.moe_norm_out(gpu_lib.make_norm(64), x, x, None, x, gpu_lib.make_norm(64), x)
     assert math.isfinite(float(x.sum()))
+
+
+def _call_under_test(B, torch, call):
+    """The call's tensors by name and a function that makes the call with them."""
+    def new(*shape, dtype=torch.float32):
+        return torch.zeros(*shape, dtype=dtype, device="cuda")
+    if call == "route":
+        r = B.make_router(64, 2)
+        t = {"logits": new(4, 64), "bias": new(64), "ids": new(4, 2, dtype=torch.int32), "w": new(4, 2)}
+        return t, lambda t: B.moe_route_groups(r, t["logits"], t["bias"], t["ids"], t["w"])
+    if call == "norm_in":
+        n = B.make_norm(64)
+        return {"x": new(4, 64), "out": new(4, 64)}, lambda t: B.moe_norm_in(n, t["x"], t["out"])
+    if call == "lora":
+        lora = B.make_lora(new(2, 4, 64, dtype=torch.bfloat16), new(2, 32, 4, dtype=torch.bfloat16))
+        t = {"x": new(4, 64), "ids": new(4, dtype=torch.int32), "base": new(4, 32), "out": new(4, 32)}
+        return t, lambda t: B.moe_lora_add(lora, t["x"], t["ids"], t["base"], t["out"])
+    n = B.make_norm(64, gate=call)
+    t = {"y": new(4, 64), "residual": new(4, 64), "gate": new(*{"channel": (64,), "token": (4,), "full": (4, 64)}[call]),
+         "out": new(4, 64), "next_out": new(4, 64)}
+    return t, lambda t: B.moe_norm_out(n, t["y"], t["residual"], t["gate"], t["out"], n, t["next_out"])
+
+
+@pytest.mark.parametrize("call", ["route", "norm_in", "channel", "token", "full", "lora"])
+def test_binding_refuses_each_wrong_tensor(gpu_lib, call):
+    torch = _torch()
+    good, run = _call_under_test(gpu_lib, torch, call)
+    run(good)
+    for name, t in good.items():
+        wide = torch.zeros(*t.shape[:-1], 2 * t.shape[-1], dtype=t.dtype, device="cuda")
+        for bad, error in ((t.to(torch.float16), TypeError), (t.to(torch.int64), TypeError),
+                           (torch.cat([t, t]), ValueError), (t[None], ValueError), (wide, ValueError),
+                           (wide[..., ::2], ValueError), (t.cpu(), ValueError)):
+            with pytest.raises(error):
+                run({**good, name: bad})
+    torch.cuda.synchronize()
+    run(good)
