@@ -191,7 +191,8 @@ moe_status moe_group_wide(const int32_t* keys, int n, int nkeys, int32_t* counts
 /* RMS norms before and after a block, with the gate and the scale on its way
  * back into the residual stream.  RMS(z; w) = z / sqrt(mean(z^2) + eps) * (weight_offset + w),
  * a NULL weight: times 1.  Sums and arithmetic in fp32 (a row whose sum of
- * squares passes fp32's range norms to 0), one rounding per output. */
+ * squares passes fp32's range norms to 0, squares below it count as 0), one
+ * rounding per output. */
 enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 };  /* none, [H], [T], [T][H] */
 enum { MOE_GATE_LINEAR = 0, MOE_GATE_SIGMOID = 1 };  /* the gate as it is, or 1 / (1 + exp(-gate)) */
 
@@ -233,6 +234,7 @@ moe_status moe_norm_out(const moe_norm* norm, const void* y, moe_dtype yt, const
  * Only the first min(ranks[a], r) rows of A[a] and columns of B[a] count.  A
  * token whose id is outside [0, num) has no adapter: out[t] = base[t].  No
  * token's result depends on another's adapter.  fp32 sums, one rounding.
+ * Infinities in an adapter reach its tokens as infinities or NaN.
  * Requests' tokens may stand in any order; long batches run best where a
  * request's tokens stand together. */
 typedef struct {

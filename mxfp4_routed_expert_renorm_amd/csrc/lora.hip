@@ -269,7 +269,7 @@ constexpr int kVStride = kMaxRank + 8;  // bf16 elements of a token's row of v p
 __device__ __forceinline__ uint16_t take_bf16(float& f) {
   const uint32_t u = __float_as_uint(f) & 0xffff0000u;
   const float rest = f - __uint_as_float(u);
-  f = rest == rest ? rest : 0.0f;  // an infinity leaves nothing over
+  f = fabsf(f) == INFINITY ? 0.0f : rest;  // an infinity leaves nothing over; a NaN, which may truncate to one, itself
   return (uint16_t)(u >> 16);
 }
 

@@ -451,6 +451,24 @@ def test_lora_a_broken_adapter_touches_only_its_tokens(gpu_lib, T):
     assert torch.equal(out[keep], want[keep]) and bool(out[1].isnan().all())
 
 
+@pytest.mark.parametrize("T", [5, 2000])
+@pytest.mark.parametrize("yt", ["f32", "bf16"])
+def test_lora_nan_of_any_payload_stays_nan(gpu_lib, T, yt):
+    """NaN whose payload lies in the bits that bf16 does not have."""
+    torch = _torch()
+    lora, x, ids, base, want = _lora_case(gpu_lib, T, 512, 256, 16, 4, "f32", yt, seed=6, ids=np.arange(T) % 4)
+    want = want.clone()
+    x.view(torch.int32)[1, 7] = 0x7F800001
+    x.view(torch.int32)[3, 500] = -1                        # 0xffffffff
+    x.view(torch.int32)[4, 0] = 0x7F800001 - (1 << 31)      # 0xff800001
+    out = torch.empty_like(base)
+    gpu_lib.moe_lora_add(lora, x, ids, base, out)
+    torch.cuda.synchronize()
+    broken = torch.zeros(T, dtype=torch.bool, device="cuda")
+    broken[[1, 3, 4]] = True
+    assert bool(out[broken].isnan().all()) and torch.equal(out[~broken], want[~broken])
+
+
 @pytest.mark.parametrize("T", [3, 80, 700])
 def test_lora_in_place_and_repeatable(gpu_lib, T):
     torch = _torch()
