@@ -8,6 +8,8 @@
 
 namespace moe {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
@@ -59,9 +61,15 @@ __device__ __forceinline__ f32x8 widen(uint4 h) {
                bf16_lo(h.z), bf16_hi(h.z), bf16_lo(h.w), bf16_hi(h.w)};
 }
 
+// fp32 -> bf16, to nearest even, NaN stays NaN: one instruction for two.  With
+// the rounding in integer steps the norms, though bound by memory, took 13.3
+// instead of 12.2 us and 28.9 instead of 27.4 (4096 x 4096).
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  return (uint32_t)f32_to_bf16(lo) | ((uint32_t)f32_to_bf16(hi) << 16);
+  const f32x2 f = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
 }
+
+__device__ __forceinline__ uint16_t bf16_of(float f) { return (uint16_t)pack2(f, 0.0f); }
 
 // Stores of results that this kernel does not read again: they leave the L2 as
 // they come instead of at the kernel's end, when all dirty lines are written back.
@@ -103,7 +111,7 @@ __device__ __forceinline__ void store8(void* p, size_t at, int n, f32x8 v) {
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (e < n) o[e] = f32_to_bf16(v[e]);
+        if (e < n) o[e] = bf16_of(v[e]);
     }
   } else {
     float* o = (float*)p + at;

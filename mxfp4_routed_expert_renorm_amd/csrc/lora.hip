@@ -183,7 +183,7 @@ __device__ __forceinline__ void token_body(const moe_lora& L, const void* __rest
       const int e = threadIdx.x + i * kTokThreads;
       if (e < m) {
         if constexpr (YBF16)
-          ((uint16_t*)out)[yt + n + e] = f32_to_bf16(y[i] + o[e]);
+          ((uint16_t*)out)[yt + n + e] = bf16_of(y[i] + o[e]);
         else
           ((float*)out)[yt + n + e] = y[i] + o[e];
       }
@@ -334,9 +334,9 @@ struct Four {
       if (n >= 4) {
         *(Packed4h*)p = Packed4h{pack2(d[0], d[1]), pack2(d[2], d[3])};
       } else {
-        if (n > 0) p[0] = f32_to_bf16(d[0]);
-        if (n > 1) p[1] = f32_to_bf16(d[1]);
-        if (n > 2) p[2] = f32_to_bf16(d[2]);
+        if (n > 0) p[0] = bf16_of(d[0]);
+        if (n > 1) p[1] = bf16_of(d[1]);
+        if (n > 2) p[2] = bf16_of(d[2]);
       }
     } else {
       d += v4f{__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]), __uint_as_float(u[3])};

@@ -10,12 +10,12 @@
 // row needs (weights and gate too) is requested before the first sum is formed.
 // Sums and everything between are fp32; each output is rounded once.
 //
-// Bound by memory: 4096 x 4096 bf16, norm_in 13.3 us (67 MB, 5.0 TB/s; a copy
-// reaches 5.1), norm_out with a channel gate and the next norm 29.0 us (134 MB,
-// 4.6 TB/s).  Large results are stored streaming: with ordinary stores the lines
+// Bound by memory: 4096 x 4096 bf16, norm_in 12.2 us (67 MB, 5.5 TB/s; a copy
+// reaches 5.1), norm_out with a channel gate and the next norm 27.4 us (134 MB,
+// 4.9 TB/s).  Large results are stored streaming: with ordinary stores the lines
 // left dirty in the L2s are written back at the kernel's end, 15.0 and 36.0 us.
-// Rows of odd width pay for stores that share lines: 509 x 2047 7.1 us, 509 x 2048
-// 5.4.  One row: 2.4 and 3.5 us, of which 1.9 are a launch.
+// Rows of odd width pay for stores that share lines: 509 x 2047 6.3 us, 509 x 2048
+// 5.2.  One row: 2.2 and 3.1 us, of which 1.9 are a launch.
 #include "chunk_dev.h"
 
 namespace moe {
