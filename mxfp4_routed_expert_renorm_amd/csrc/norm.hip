@@ -10,12 +10,12 @@
 // row needs (weights and gate too) is requested before the first sum is formed.
 // Sums and everything between are fp32; each output is rounded once.
 //
-// Bound by memory: 4096 x 4096 bf16, norm_in 12.2 us (67 MB, 5.5 TB/s; a copy
-// reaches 5.1), norm_out with a channel gate and the next norm 27.4 us (134 MB,
-// 4.9 TB/s).  Large results are stored streaming: with ordinary stores the lines
-// left dirty in the L2s are written back at the kernel's end, 15.0 and 36.0 us.
-// Rows of odd width pay for stores that share lines: 509 x 2047 6.3 us, 509 x 2048
-// 5.2.  One row: 2.2 and 3.1 us, of which 1.9 are a launch.
+// Bound by memory: 4096 x 4096 bf16, norm_in 12.0 us (67 MB, 5.6 TB/s; a copy
+// reaches 5.1), norm_out with a channel gate and the next norm 24.4 us (134 MB,
+// 5.5 TB/s).  Large results are stored streaming: with ordinary stores the lines
+// left dirty in the L2s are written back at the kernel's end, 13.3 and 28.2 us.
+// Rows of odd width pay for stores that share lines: 509 x 2047 6.2 us, 509 x 2048
+// 4.5.  One row: 2.2 and 3.1 us, of which 1.9 are a launch.
 #include "chunk_dev.h"
 
 namespace moe {
@@ -72,101 +72,133 @@ __global__ __launch_bounds__(1024) void norm_in_kernel(NormArgs a) {
   }
 }
 
-template <bool YBF16, bool RBF16, bool NBF16, int V>
+// LOOP: as many workgroups as the chip holds at a time go over the rows, with the
+// weights and a channel gate in registers throughout (read again for every row,
+// from the caches, they are nearly as many bytes as the row's own).  4096 rows of
+// 4096 24.3 instead of 27.5 us, 1200 rows 8.6 instead of 10.8, 1500 of 5120 13.7
+// instead of 18.1; the same for norm_in gained 4% at 4096 rows and lost 18% at 1200,
+// so its rows stay one a group of threads.
+template <bool YBF16, bool RBF16, bool NBF16, int V, bool LOOP>
 __global__ __launch_bounds__(1024) void norm_out_kernel(NormArgs a) {
-  __shared__ float red[2][16];
-  const int in_row = threadIdx.x & (a.per_row - 1);
-  const int row = blockIdx.x * (blockDim.x / a.per_row) + threadIdx.x / a.per_row;
-  const bool live = row < a.T;
-  const size_t at = (size_t)min(row, a.T - 1) * a.H;
-  f32x8 y[V], r[V], w[V], g[V], nw[V];
+  __shared__ float red[LOOP ? 2 : 1][2][16];
+  const int in_row = threadIdx.x & (a.per_row - 1), rows = blockDim.x / a.per_row;
   const bool elementwise = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL;
-  float tok = 1.f;
-  if (a.gate_kind == MOE_GATE_TOKEN) tok = load1(a.gate, a.gbf, min(row, a.T - 1));
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
+  int row0 = blockIdx.x * rows, turn = 0;
+  f32x8 y[V], r[V], w[V], g[V], nw[V];
+  auto load_weights = [&](int i) {
     const int e = (i * a.per_row + in_row) * 8, n = a.H - e;
-    y[i] = load8<YBF16>(a.y, at + e, n);
-    r[i] = load8<RBF16>(a.residual, at + e, n);
-    g[i] = elementwise ? load8_raw(a.gate, a.gbf, a.gate_kind == MOE_GATE_FULL ? at + e : e, n) : f32x8(0.f);
     w[i] = a.post && a.post_w ? load8_raw(a.post_w, a.wbf, e, n) : f32x8(0.f);
     nw[i] = a.next_out && a.pre_w ? load8_raw(a.pre_w, a.nwbf, e, n) : f32x8(0.f);
-  }
-  float c = a.alpha;
-  if (a.post) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(y[i][j], y[i][j], ss);
-    const float rs = rsqrtf(fmaf(row_sum(ss, a.per_row, red[0]), a.inv_h, a.eps));
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      y[i] *= rs;
-      if (a.post_w) y[i] *= a.offset + widen_raw(w[i], a.wbf);
-    }
-  }
-  if (a.gate_kind == MOE_GATE_TOKEN) c *= a.sigmoid ? sigmoid(tok) : tok;
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (elementwise) {
-      f32x8 f = widen_raw(g[i], a.gbf);
-      if (a.sigmoid) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = sigmoid(f[j]);
-      }
-      y[i] *= f;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      r[i][j] = fmaf(c, y[i][j], r[i][j]);
-      ss = fmaf(r[i][j], r[i][j], ss);
-    }
-  }
-  if (live) {
+  };
+  if constexpr (LOOP) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = (i * a.per_row + in_row) * 8;
-      store8<RBF16, V == 2>(a.out, at + e, a.H - e, r[i]);
+      g[i] = a.gate_kind == MOE_GATE_CHANNEL ? load8_raw(a.gate, a.gbf, e, a.H - e) : f32x8(0.f);
+      load_weights(i);
     }
   }
-  if (!a.next_out) return;
-  const float rs = rsqrtf(fmaf(row_sum(ss, a.per_row, red[1]), a.inv_h, a.next_eps));
-  if (!live) return;
+  do {
+    const int row = row0 + threadIdx.x / a.per_row;
+    const bool live = row < a.T;
+    const size_t at = (size_t)min(row, a.T - 1) * a.H;
+    float tok = 1.f;
+    if (a.gate_kind == MOE_GATE_TOKEN) tok = load1(a.gate, a.gbf, min(row, a.T - 1));
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = (i * a.per_row + in_row) * 8;
-    r[i] *= rs;
-    if (a.pre_w) r[i] *= a.next_offset + widen_raw(nw[i], a.nwbf);
-    store8<NBF16, V == 2>(a.next_out, at + e, a.H - e, r[i]);
-  }
+    for (int i = 0; i < V; ++i) {
+      const int e = (i * a.per_row + in_row) * 8, n = a.H - e;
+      y[i] = load8<YBF16>(a.y, at + e, n);
+      r[i] = load8<RBF16>(a.residual, at + e, n);
+      if constexpr (LOOP) {
+        if (a.gate_kind == MOE_GATE_FULL) g[i] = load8_raw(a.gate, a.gbf, at + e, n);
+      } else {
+        g[i] = elementwise ? load8_raw(a.gate, a.gbf, a.gate_kind == MOE_GATE_FULL ? at + e : e, n) : f32x8(0.f);
+        load_weights(i);
+      }
+    }
+    float c = a.alpha;
+    if (a.post) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(y[i][j], y[i][j], ss);
+      const float rs = rsqrtf(fmaf(row_sum(ss, a.per_row, red[turn][0]), a.inv_h, a.eps));
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        y[i] *= rs;
+        if (a.post_w) y[i] *= a.offset + widen_raw(w[i], a.wbf);
+      }
+    }
+    if (a.gate_kind == MOE_GATE_TOKEN) c *= a.sigmoid ? sigmoid(tok) : tok;
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (elementwise) {
+        f32x8 f = widen_raw(g[i], a.gbf);
+        if (a.sigmoid) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = sigmoid(f[j]);
+        }
+        y[i] *= f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        r[i][j] = fmaf(c, y[i][j], r[i][j]);
+        ss = fmaf(r[i][j], r[i][j], ss);
+      }
+    }
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = (i * a.per_row + in_row) * 8;
+        store8<RBF16, V == 2>(a.out, at + e, a.H - e, r[i]);
+      }
+    }
+    if (a.next_out) {
+      const float rs = rsqrtf(fmaf(row_sum(ss, a.per_row, red[turn][1]), a.inv_h, a.next_eps));
+      if (!live) break;  // only in the last turn
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = (i * a.per_row + in_row) * 8;
+        r[i] *= rs;
+        if (a.pre_w) r[i] *= a.next_offset + widen_raw(nw[i], a.nwbf);
+        store8<NBF16, V == 2>(a.next_out, at + e, a.H - e, r[i]);
+      }
+    }
+    if (LOOP) turn ^= 1;
+  } while (LOOP && (row0 += gridDim.x * rows) < a.T);
 }
 
 struct Shape {
   dim3 grid, block;
   int v;
+  bool loop;
 };
 
-// One chunk a thread up to 2^21 elements, where a row's latency counts, two (and
-// streaming stores) above, where bandwidth does.  norm_in at H = 4096 with one and
-// two: 1 row 2.5 and 2.9 us, 256 rows 3.0 and 3.3, 512 rows 3.5 and 3.5, 1024 rows
-// 5.2 and 4.1, 4096 rows 15.2 and 13.0; 1024 x 2048 3.5 and 3.6; norm_out at
-// H = 4096: 1 row 3.6 and 4.8, 512 rows 5.9 and 5.8, 4096 rows 34.2 and 28.7.
-Shape shape(NormArgs& a) {
+constexpr int kCUs = 256;
+
+// One chunk a thread up to 2^20 elements, where a row's latency counts, two (and
+// streaming stores) above, where bandwidth does.  H = 4096, with one and two:
+// norm_in 1 row 2.2 and 2.4 us, 256 rows 2.7 and 2.8, 512 rows 3.15 and 3.05, 1024
+// rows 4.7 and 3.7, 4096 rows 14.1 and 12.0; norm_out 1 row 3.1 and 4.0, 256 rows 3.9
+// and 4.7, 512 rows 5.2 and 5.0, 1024 rows 9.3 and 8.1, 4096 rows 31.4 and 24.4.
+Shape shape(NormArgs& a, bool may_loop) {
   const int chunks = (a.H + 7) / 8;
-  const int v = chunks > 1024 || (size_t)a.T * a.H > (size_t)1 << 21 ? 2 : 1;
+  const int v = chunks > 1024 || (size_t)a.T * a.H > (size_t)1 << 20 ? 2 : 1;
   int per = 64;
   while (per * v < chunks) per *= 2;
   const int block = max(per, 256), rows = block / per;
   a.per_row = per;
   a.inv_h = 1.0f / (float)a.H;
-  return {dim3((a.T + rows - 1) / rows), dim3(block), v};
+  const int blocks = (a.T + rows - 1) / rows, resident = kCUs * 1024 / block;
+  const bool loop = may_loop && v == 2 && blocks > resident;
+  return {dim3(loop ? resident : blocks), dim3(block), v, loop};
 }
 
 template <bool XB, bool OB>
 void run_in(NormArgs& a, hipStream_t s) {
-  const Shape h = shape(a);
+  const Shape h = shape(a, false);
   if (h.v == 1)
     launch(MOE_PROF_NORM, norm_in_kernel<XB, OB, 1>, h.grid, h.block, 0, s, a);
   else
@@ -175,11 +207,13 @@ void run_in(NormArgs& a, hipStream_t s) {
 
 template <bool YB, bool RB, bool NB>
 void run_out(NormArgs& a, hipStream_t s) {
-  const Shape h = shape(a);
+  const Shape h = shape(a, true);
   if (h.v == 1)
-    launch(MOE_PROF_NORM, norm_out_kernel<YB, RB, NB, 1>, h.grid, h.block, 0, s, a);
+    launch(MOE_PROF_NORM, norm_out_kernel<YB, RB, NB, 1, false>, h.grid, h.block, 0, s, a);
+  else if (!h.loop)
+    launch(MOE_PROF_NORM, norm_out_kernel<YB, RB, NB, 2, false>, h.grid, h.block, 0, s, a);
   else
-    launch(MOE_PROF_NORM, norm_out_kernel<YB, RB, NB, 2>, h.grid, h.block, 0, s, a);
+    launch(MOE_PROF_NORM, norm_out_kernel<YB, RB, NB, 2, true>, h.grid, h.block, 0, s, a);
 }
 
 }  // namespace

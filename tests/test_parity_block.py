@@ -232,6 +232,42 @@ def test_norm_many_rows(gpu_lib):
     assert float(((out.check().double() - ref).abs() / ref.abs().clamp_min(1e-30)).max()) <= _c(H) * U + U
 
 
+@pytest.mark.parametrize("T,H", [(20001, 96), (2501, 2047), (1100, 4096), (300, 16383)])
+@pytest.mark.parametrize("kind,act", [("none", "none"), ("channel", "sigmoid"), ("token", "none"), ("full", "none")])
+def test_norm_out_more_rows_than_the_chip_holds(gpu_lib, T, H, kind, act):
+    """Workgroups that take several rows, the last turn ragged: every row against
+    float64, a broken row alone, in place, without the next norm or the post norm."""
+    torch = _torch()
+    rng = np.random.default_rng(T)
+    eps = float(np.float32(1e-5))
+    y, res = _up(rng.standard_normal((T, H)), "bf16", 1), _up(rng.standard_normal((T, H)) * 2, "bf16")
+    gshape = {"none": None, "channel": (H,), "token": (T,), "full": (T, H)}[kind]
+    gate = None if gshape is None else _up(rng.standard_normal(gshape), "bf16")
+    w = _up(rng.standard_normal(H), "bf16")
+    for post in (True, False):
+        norm = gpu_lib.make_norm(H, 1e-5, pre=w, post=w, post_norm=post, gate=kind, gate_act=act, alpha=0.5)
+        out, nout, alone = Guarded((T, H), "bf16"), Guarded((T, H), "f32", 1), Guarded((T, H), "bf16")
+        gpu_lib.moe_norm_out(norm, y, res, gate, out.t, norm, nout.t)
+        gpu_lib.moe_norm_out(norm, y, res, gate, alone.t)
+        a, b = y.clone(), res.clone()
+        gpu_lib.moe_norm_out(norm, a, b, gate, b, norm, a)
+        torch.cuda.synchronize()
+        ref, tol, nref, ntol = _norm_out_ref(_f64(y), _f64(res), None if gate is None else _f64(gate), _f64(w), _f64(w),
+                                             kind, act, 0.5, post, 0.0, eps, torch.bfloat16, torch.float32)
+        _close(_f64(out.check()), ref, tol, "out")
+        _close(_f64(nout.check()), nref, ntol, "next")
+        assert torch.equal(alone.check(), out.t) and torch.equal(b, out.t) and torch.equal(a, nout.t.bfloat16())
+        bad = y.clone()
+        bad[T - 1, 3], bad[5, H - 1] = float("nan"), float("inf")
+        a, b = torch.empty_like(res), torch.empty(T, H, device="cuda")
+        gpu_lib.moe_norm_out(norm, bad, res, gate, a, norm, b)
+        torch.cuda.synchronize()
+        keep = torch.ones(T, dtype=torch.bool, device="cuda")
+        keep[[5, T - 1]] = False
+        assert torch.equal(a[keep], out.t[keep]) and torch.equal(b[keep], nout.t[keep])
+        assert bool(a[T - 1, 3].isnan()) and not bool(a[5, H - 1].isfinite()) and bool(b[T - 1].isnan().all())
+
+
 # ---------------------------------------------------------------------- routing
 
 def _route(gpu_lib, logits, k, bias=None, lt="f32", shift=0, **kw):
