@@ -38,7 +38,7 @@ __device__ __forceinline__ int rank_of(const moe_lora& L, int id) {
 // and the reductions.  That chain bounds small calls (K = N = 4096, rank 16, one
 // token: 4.3 us, of which 1.9 are a launch); larger ranks are bound by what one
 // compute unit draws (rank 64, 64 tokens of 64 adapters: 16.8 us, 67 MB, 4.0 TB/s;
-// with ranks 8 to 64 mixed the tokens of rank 64 set the pace: 17.3 us).
+// with ranks 8 to 64 mixed the tokens of rank 64 set the pace: 17.1 us).
 
 constexpr int kTokThreads = 512, kTokWaves = kTokThreads / 64;
 constexpr int kTokOut = 1024;  // outputs gathered in LDS before they are written
@@ -257,9 +257,9 @@ __global__ __launch_bounds__(kTokThreads, WIDE ? 2 : 4) void token_kernel(moe_lo
 // so one adapter's NaN cannot reach another's tokens.
 //
 // Large calls are bound by memory: 4096 tokens, K = N = 4096, rank 32, bf16, one
-// request: 24.0 us, 4.2 TB/s over x, base, out and the adapter (5.1 is a copy's
+// request: 23.4 us, 4.3 TB/s over x, base, out and the adapter (5.1 is a copy's
 // rate).  A tile at the border of two requests takes longer than the others, and
-// at 4096 tokens every compute unit has one tile: twelve requests 30.3 us.
+// at 4096 tokens every compute unit has one tile: twelve requests 29.7 us.
 
 constexpr int kTileWaves = 8, kTileThreads = 64 * kTileWaves;
 constexpr int kMaxPass = 8;             // most tasks per pass over x
