@@ -246,9 +246,10 @@ __global__ __launch_bounds__(kTokThreads, WIDE ? 2 : 4) void token_kernel(moe_lo
 //
 // A x: first operand the rows of A (16 of them a "task": one adapter, 16 of its
 // ranks), second the tokens; the wavefronts split K in slabs of 64 and their
-// parts meet in LDS.  The sum of a token's own adapter is split into bf16 parts
-// whose sum is the fp32 value (two parts, off by at most 2^-16 of it, for bf16
-// outputs; three, exact, for fp32), so the second product runs on bf16 operands.
+// parts meet in LDS.  The sum of a token's own adapter is split as fp32 inputs are,
+// so the second product runs on bf16 operands and loses nothing of it, for bf16
+// outputs too: two parts cut below 2^-15 of it, always towards 0, and a base that
+// cancels the sum's upper bits leaves little else.
 //
 // B v: first operand the tokens' parts, second 16 outputs.  Column m of product q
 // stands for output 4 m + q of a block of 64, so that four products leave four
@@ -264,6 +265,7 @@ __global__ __launch_bounds__(kTokThreads, WIDE ? 2 : 4) void token_kernel(moe_lo
 constexpr int kTileWaves = 8, kTileThreads = 64 * kTileWaves;
 constexpr int kMaxPass = 8;             // most tasks per pass over x
 constexpr int kVStride = kMaxRank + 8;  // bf16 elements of a token's row of v parts
+constexpr int kParts = 3;               // bf16 parts of an fp32 value
 
 // fp32 -> bf16 by truncation: what is left over is exact
 __device__ __forceinline__ uint16_t take_bf16(float& f) {
@@ -357,7 +359,7 @@ struct Four {
 template <bool XBF16>
 struct XSlab {
   static constexpr int kX = XBF16 ? 2 : 4;                                  // pieces a lane
-  static constexpr int kParts = XBF16 ? 1 : 3, kBytes = kParts * 16 * 128;  // bf16 parts of an element in LDS
+  static constexpr int kXParts = XBF16 ? 1 : kParts, kBytes = kXParts * 16 * 128;  // bf16 parts of an element in LDS
   uint4 x[kX];
 
   template <bool FULL>
@@ -394,7 +396,7 @@ struct XSlab {
         char* to = lds + row * 128 + ((c >> 1) ^ (row & 7)) * 16 + (c & 1) * 8;
         float f[4] = {__uint_as_float(x[i].x), __uint_as_float(x[i].y), __uint_as_float(x[i].z), __uint_as_float(x[i].w)};
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
+        for (int p = 0; p < kParts; ++p) {
           const uint32_t h0 = take_bf16(f[0]), h1 = take_bf16(f[1]), h2 = take_bf16(f[2]), h3 = take_bf16(f[3]);
           *(uint2*)(to + p * 2048) = make_uint2(h0 | (h1 << 16), h2 | (h3 << 16));
         }
@@ -450,14 +452,14 @@ __device__ __forceinline__ void slab_product(const XSlab<XBF16>& x, const ASlab<
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int at = ((h * 4 + g) ^ (col & 7)) * 16;
-    v8bf xv[XSlab<XBF16>::kParts];
+    v8bf xv[XSlab<XBF16>::kXParts];
 #pragma unroll
-    for (int i = 0; i < XSlab<XBF16>::kParts; ++i) xv[i] = *(const v8bf*)(xl + i * 2048 + at);
+    for (int i = 0; i < XSlab<XBF16>::kXParts; ++i) xv[i] = *(const v8bf*)(xl + i * 2048 + at);
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       const v8bf av = *(const v8bf*)(al + p * 2048 + at);
 #pragma unroll
-      for (int i = 0; i < XSlab<XBF16>::kParts; ++i)
+      for (int i = 0; i < XSlab<XBF16>::kXParts; ++i)
         acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xv[i], acc[p], 0, 0, 0);
     }
   }
@@ -560,15 +562,14 @@ struct Pieces {
 };
 
 // the products of a step's pieces with the parts of v
-template <int NS>
-__device__ __forceinline__ void multiply(const Step& s, const uint16_t (&vs)[NS][16][kVStride], const char* lds,
+__device__ __forceinline__ void multiply(const Step& s, const uint16_t (&vs)[kParts][16][kVStride], const char* lds,
                                          v4f (&d)[4]) {
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   v8bf bv[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) bv[q] = *(const v8bf*)(lds + (q * 16 + col) * 64 + (g ^ ((col >> 1) & 3)) * 16);
 #pragma unroll
-  for (int m = 0; m < NS; ++m) {
+  for (int m = 0; m < kParts; ++m) {
     const v8bf vv = *(const v8bf*)&vs[m][col][(s.j0 + g) * 8];
 #pragma unroll
     for (int q = 0; q < 4; ++q) d[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, bv[q], d[q], 0, 0, 0);
@@ -602,10 +603,10 @@ __device__ __forceinline__ void store_sum(const Four<YBF16> (&y)[4], bool based,
 // unconditional, so the pieces of the next G steps (fetched as soon as the last
 // have gone to LDS) and the next block's base stay in flight meanwhile.
 // `ready` is called once the first loads are under way: v is there after it.
-template <int NS, bool YBF16, int G, bool ONCE, class Ready>
+template <bool YBF16, int G, bool ONCE, class Ready>
 __device__ __forceinline__ void blocks(Ready&& ready, const moe_lora& L, const Step* list, int steps,
                                        const int (&slot)[4], const size_t (&row)[4],
-                                       const uint16_t (&vs)[NS][16][kVStride], int nb, int n1, const void* base,
+                                       const uint16_t (&vs)[kParts][16][kVStride], int nb, int n1, const void* base,
                                        bool based, void* out, char* lds) {
   const int n = (threadIdx.x & 15) * 4, r = L.r;
   Four<YBF16> y[4], y_next[4];
@@ -637,7 +638,7 @@ __device__ __forceinline__ void blocks(Ready&& ready, const moe_lora& L, const S
 #pragma unroll
             for (int q = 0; q < 4; ++q) d[q] = v4f{0.f, 0.f, 0.f, 0.f};
           }
-          multiply<NS>(s[g], vs, lds, d);
+          multiply(s[g], vs, lds, d);
           take(s[g], slot, d, acc);
         }
       }
@@ -652,11 +653,10 @@ template <bool XBF16, bool YBF16>
 __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const void* __restrict__ x, int T,
                                                             const int32_t* __restrict__ ids, const void* base,
                                                             void* out, int per, int split, int work) {
-  constexpr int NS = YBF16 ? 2 : 3;
   // tasks per pass over x, and a wavefront's LDS for them: x 2 or 6 KB, A 2 KB a task (later a slab of B)
   constexpr int kPass = XBF16 ? 8 : 4, kStage = XSlab<XBF16>::kBytes + kPass * 2048;
   __shared__ __align__(16) char stage[kTileWaves][kStage];
-  __shared__ __align__(16) uint16_t vs[NS][16][kVStride];
+  __shared__ __align__(16) uint16_t vs[kParts][16][kVStride];
   __shared__ int tok_slot[16], ad_id[16], ad_rank[16], n_task, n_step;
   __shared__ float ad_scale[16];
   __shared__ uint8_t task_slot[128], task_tile[128];
@@ -735,7 +735,7 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
         s *= ad_scale[slot];
         if (j >= ad_rank[slot]) s = 0.f;
 #pragma unroll
-        for (int n = 0; n < NS; ++n) vs[n][tok][j] = take_bf16(s);
+        for (int n = 0; n < kParts; ++n) vs[n][tok][j] = take_bf16(s);
       }
     }
     __syncthreads();
@@ -789,7 +789,7 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
     const int whole = r % 8 == 0 ? n1 / 64 * 64 : max(0, min(n1, N - 7)) / 64 * 64;
     const void* from = based ? base : out;
     auto run = [&](auto g, auto once) {
-      blocks<NS, YBF16, decltype(g)::value, decltype(once)::value>(last, L, step, steps, slot, row, vs, nb, whole, from,
+      blocks<YBF16, decltype(g)::value, decltype(once)::value>(last, L, step, steps, slot, row, vs, nb, whole, from,
                                                                    based, out, lds);
     };
     using yes = std::true_type;
@@ -823,7 +823,7 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
 #pragma unroll
         for (int q = 0; q < 4; ++q) d[q] = v4f{0.f, 0.f, 0.f, 0.f};
       }
-      multiply<NS>(s, vs, lds, d);
+      multiply(s, vs, lds, d);
       take(s, slot, d, acc);
     }
 #pragma unroll
