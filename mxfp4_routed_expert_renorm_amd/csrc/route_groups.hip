@@ -179,6 +179,11 @@ __device__ __forceinline__ void write_picks(const moe_router& R, uint64_t picks,
   }
 }
 
+// a softmax's exponential in double precision; a masked expert's is 0 (NaN too)
+__device__ __forceinline__ double soft_exp(float l, float top) {
+  return !(l > kLowest) ? 0.0 : l == top ? 1.0 : exp((double)l - (double)top);
+}
+
 template <int EPL>
 __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R, int T, uint32_t inv_gs,
                                                                    const void* __restrict__ logits, bool lbf16,
@@ -212,7 +217,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
   float* my_w = w + (size_t)t * R.k;
 
   if (sigmoid_scores || (!bias && top > kLowest && top < INFINITY)) {
-    float c[EPL], sum = 0.f;
+    float c[EPL];
     bool wide = false;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
@@ -222,9 +227,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
         wide |= live && fabsf(b[j]) > kMaxBias;
         c[j] = live && c[j] == c[j] ? c[j] : -INFINITY;
       } else {
-        c[j] = __expf(l[j] - top);
-        sum += live && lane + 64 * j < E ? c[j] : 0.f;
-        c[j] = live ? c[j] : -INFINITY;
+        c[j] = live ? __expf(l[j] - top) : -INFINITY;
       }
     }
     bool sure = __ballot(wide) == 0;
@@ -283,7 +286,14 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
           }
           picks = __ballot(lane < n && before < R.k);
         }
-        write_picks(R, picks, e, s, sigmoid_scores ? 1.0 : (double)wave_sum(sum), my_ids, my_w);
+        double over = 1.0;
+        if (!sigmoid_scores && !R.renorm) {  // the weights' denominator: every expert's exponential
+          over = 0.0;
+#pragma unroll
+          for (int j = 0; j < EPL; ++j) over += lane + 64 * j < E ? soft_exp(l[j], top) : 0.0;
+          over = wave_sum_f64(over);
+        }
+        write_picks(R, picks, e, s, over, my_ids, my_w);
         return;
       }
     }
@@ -298,7 +308,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      s[j] = !(l[j] > kLowest) ? 0.0 : l[j] == top ? 1.0 : exp((double)l[j] - (double)top);
+      s[j] = soft_exp(l[j], top);
       sum += lane + 64 * j < E ? s[j] : 0.0;
     }
     sum = wave_sum_f64(sum);
