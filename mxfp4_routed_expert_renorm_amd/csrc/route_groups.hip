@@ -115,9 +115,11 @@ __device__ __forceinline__ float readlane_any(float v, int lane) {
 __device__ __forceinline__ double readlane_any(double v, int lane) { return readlane_f64(v, lane); }
 
 // The groups that stay, a bit each, from the choices (-inf: masked).  last: the
-// value of the last that stays; apart: how far it is above the best that does not.
+// value of the last that stays; apart: how far it is above the best that does not;
+// near: whether a group's value is within kApart of it without being equal.
 template <class F, int EPL>
-__device__ __forceinline__ uint64_t best_groups(const moe_router& R, const F (&c)[EPL], F* lds, F* last, F* apart) {
+__device__ __forceinline__ uint64_t best_groups(const moe_router& R, const F (&c)[EPL], F* lds, F* last, F* apart,
+                                                bool* near) {
   const int lane = threadIdx.x & 63, gs = R.E / R.groups;
   const F inf = (F)INFINITY;
   int per = 64;  // lanes a group: a power of two
@@ -149,6 +151,7 @@ __device__ __forceinline__ uint64_t best_groups(const moe_router& R, const F (&c
   const uint64_t kept = __ballot(leads && rank < R.topk_groups);
   *last = readlane_any(value, __ffsll((unsigned long long)__ballot(leads && rank == R.topk_groups - 1)) - 1);
   *apart = *last - readlane_any(value, __ffsll((unsigned long long)__ballot(leads && rank == R.topk_groups)) - 1);
+  *near = __ballot(leads && value != *last && fabs(value - *last) <= (F)kApart) != 0;
   if (per == 1) return kept;
   uint64_t stay = 0;
   for (int i = 0; i < R.groups; ++i) stay |= ((kept >> (i * per)) & 1) << i;
@@ -234,15 +237,17 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
     uint64_t stay = ~0ull;
     if (sure && R.topk_groups < R.groups) {
       float last, apart;
+      bool near;
       if (!sigmoid_scores && R.group_score == MOE_GROUP_MAX) {
-        // by the logits themselves, whose ties are ties of the scores; down to where scores underflow
+        // by the logits themselves, down to where scores underflow.  Ties of logits are ties of the
+        // scores, but scores also tie where logits differ by less than a double exponential shows.
         float v[EPL];
 #pragma unroll
         for (int j = 0; j < EPL; ++j) v[j] = l[j] > kLowest ? l[j] : -INFINITY;
-        stay = best_groups<float, EPL>(R, v, (float*)choice[wave], &last, &apart);
-        sure = last > top - 700.f && (apart == 0.f || apart > kApart);
+        stay = best_groups<float, EPL>(R, v, (float*)choice[wave], &last, &apart, &near);
+        sure = last > top - 700.f && (apart == 0.f ? !near : apart > kApart);
       } else {
-        stay = best_groups<float, EPL>(R, c, (float*)choice[wave], &last, &apart);
+        stay = best_groups<float, EPL>(R, c, (float*)choice[wave], &last, &apart, &near);
         sure = apart > kGroupsApart;
       }
     }
@@ -325,8 +330,9 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
   uint64_t stay = ~0ull;  // groups
   if (R.topk_groups < R.groups) {
     double last, apart;
+    bool near;
     wave_turn();
-    stay = best_groups<double, EPL>(R, c, choice[wave], &last, &apart);
+    stay = best_groups<double, EPL>(R, c, choice[wave], &last, &apart, &near);
   }
 
   // images: 0 for what is no candidate

@@ -37,3 +37,22 @@ def test_route_weights_to_one_rounding(gpu_lib, E, k, scoring):
                 got, w, want, ww = _route(gpu_lib, lg, k, scoring=scoring, renorm=renorm, scale=2.5, **kw)
                 assert np.array_equal(got, want), kw
                 _close(w, ww, np.abs(ww) * (U + (E + 8) * 2.0 ** -53) + 2.0 ** -150, f"weights {renorm} {std} {kw}")
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_groups_tied_in_double_but_not_as_logits(gpu_lib, renorm):
+    """Softmax, groups by their best score: best logits within the rounding of a
+    double exponential are equal scores, and the lower group stays."""
+    tiny = 1e-20
+    best = [  # per row, the best logit of each of four groups
+        (-tiny, 0.0, 0.0, -3.0), (0.0, 0.0, tiny, -3.0), (-2.0, -tiny, 0.0, 0.0), (-tiny, 0.0, -tiny, 0.0),
+        (0.0, tiny, 0.0, tiny), (-3.0, -2 * tiny, -tiny, 0.0), (0.0, 0.0, 0.0, 0.0), (-1e-6, 0.0, 0.0, 0.0),
+        (0.0, 0.0, 1e-6, -1e-6), (1.0, 1.0, 1.0, 1.0 + 2.0 ** -23), (1e-30, -1e-30, 0.0, 0.0)]
+    lg = np.full((len(best), 32), -5.0, np.float32)
+    for t, row in enumerate(best):
+        lg[t, 3::8] = row
+    for kept in (1, 2, 3):
+        for k in (1, 4):
+            got, _, want, _ = _route(gpu_lib, lg, k, scoring="softmax", groups=4, topk_groups=kept, group_score="max",
+                                     renorm=renorm)
+            assert np.array_equal(got, want), (kept, k, np.argwhere((got != want).any(1)).ravel())
