@@ -315,40 +315,44 @@ struct Four {
     }
   }
 
-  // d, and what was loaded if `based`
-  __device__ __forceinline__ void store_all(void* out, size_t at, bool based, v4f d) const {
+  // d and what was loaded, in one rounding; `keep`: the bits that were loaded
+  __device__ __forceinline__ void add(v4f d, bool keep) {
     if constexpr (YBF16) {
-      const uint32_t a = based ? u[0] : 0, b = based ? u[1] : 0;
-      d += v4f{bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b)};
-      stream4h((uint16_t*)out + at, make_uint2(pack2(d[0], d[1]), pack2(d[2], d[3])));
+      d += v4f{bf16_lo(u[0]), bf16_hi(u[0]), bf16_lo(u[1]), bf16_hi(u[1])};
+      u[0] = keep ? u[0] : pack2(d[0], d[1]);
+      u[1] = keep ? u[1] : pack2(d[2], d[3]);
     } else {
-      const v4f b = {__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]), __uint_as_float(u[3])};
-      d = based ? d + b : d;
-      stream4f((float*)out + at, d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = keep ? u[i] : __float_as_uint(d[i] + __uint_as_float(u[i]));
     }
   }
 
-  // + d, rounded once
-  __device__ __forceinline__ void store(void* out, size_t at, int n, v4f d) const {
+  __device__ __forceinline__ void store_all(void* out, size_t at) const {
+    if constexpr (YBF16)
+      stream4h((uint16_t*)out + at, make_uint2(u[0], u[1]));
+    else
+      stream4f((float*)out + at, f32x4{__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]),
+                                       __uint_as_float(u[3])});
+  }
+
+  __device__ __forceinline__ void store(void* out, size_t at, int n) const {
     if constexpr (YBF16) {
-      d += v4f{bf16_lo(u[0]), bf16_hi(u[0]), bf16_lo(u[1]), bf16_hi(u[1])};
       uint16_t* p = (uint16_t*)out + at;
       if (n >= 4) {
-        *(Packed4h*)p = Packed4h{pack2(d[0], d[1]), pack2(d[2], d[3])};
+        *(Packed4h*)p = Packed4h{u[0], u[1]};
       } else {
-        if (n > 0) p[0] = bf16_of(d[0]);
-        if (n > 1) p[1] = bf16_of(d[1]);
-        if (n > 2) p[2] = bf16_of(d[2]);
+        if (n > 0) p[0] = (uint16_t)u[0];
+        if (n > 1) p[1] = (uint16_t)(u[0] >> 16);
+        if (n > 2) p[2] = (uint16_t)u[1];
       }
     } else {
-      d += v4f{__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]), __uint_as_float(u[3])};
-      float* p = (float*)out + at;
+      uint32_t* p = (uint32_t*)out + at;
       if (n >= 4) {
-        *(Packed4f*)p = Packed4f{d[0], d[1], d[2], d[3]};
+        *(Packed4f*)p = Packed4f{__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]), __uint_as_float(u[3])};
       } else {
-        if (n > 0) p[0] = d[0];
-        if (n > 1) p[1] = d[1];
-        if (n > 2) p[2] = d[2];
+        if (n > 0) p[0] = u[0];
+        if (n > 1) p[1] = u[1];
+        if (n > 2) p[2] = u[2];
       }
     }
   }
@@ -590,11 +594,16 @@ __device__ __forceinline__ void load_base(Four<YBF16> (&y)[4], const void* base,
   for (int i = 0; i < 4; ++i) y[i].load_all(base, row[i] + n);
 }
 
+// tokens without an adapter (slot -1) keep the base's bits
 template <bool YBF16>
-__device__ __forceinline__ void store_sum(const Four<YBF16> (&y)[4], bool based, void* out, const size_t (&row)[4],
-                                          int n, const v4f (&acc)[4]) {
+__device__ __forceinline__ void store_sum(Four<YBF16> (&y)[4], bool based, const int (&slot)[4], void* out,
+                                          const size_t (&row)[4], int n, const v4f (&acc)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) y[i].store_all(out, row[i] + n, based, v4f{acc[0][i], acc[1][i], acc[2][i], acc[3][i]});
+  for (int i = 0; i < 4; ++i) {
+    if (!based) y[i] = {};
+    y[i].add(v4f{acc[0][i], acc[1][i], acc[2][i], acc[3][i]}, slot[i] < 0);
+    y[i].store_all(out, row[i] + n);
+  }
 }
 
 // The second product over whole blocks of 64 outputs, every kTileWaves-th from nb
@@ -643,7 +652,7 @@ __device__ __forceinline__ void blocks(Ready&& ready, const moe_lora& L, const S
         }
       }
     }
-    store_sum(y, based, out, row, nb + n, acc);
+    store_sum(y, based, slot, out, row, nb + n, acc);
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = y_next[i];
   }
@@ -686,6 +695,7 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
     if (lane < 16) id = ids[min(t0 + lane, T - 1)];  // past the end: the last token again
     has = lane < 16 && id >= 0 && id < L.num;
     if (has) rank = rank_of(L, id);
+    has = rank > 0;  // an adapter of no rank is none
     if (has && L.scale) scale = L.scale[id];
   }
   ax.begin();
@@ -827,8 +837,10 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
       take(s, slot, d, acc);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      y[i].store(out, row[i] + nb + col * 4, N - nb - col * 4, v4f{acc[0][i], acc[1][i], acc[2][i], acc[3][i]});
+    for (int i = 0; i < 4; ++i) {
+      y[i].add(v4f{acc[0][i], acc[1][i], acc[2][i], acc[3][i]}, slot[i] < 0);
+      y[i].store(out, row[i] + nb + col * 4, N - nb - col * 4);
+    }
   }
 }
 
