@@ -596,11 +596,10 @@ __device__ __forceinline__ void load_base(Four<YBF16> (&y)[4], const void* base,
 
 // tokens without an adapter (slot -1) keep the base's bits
 template <bool YBF16>
-__device__ __forceinline__ void store_sum(Four<YBF16> (&y)[4], bool based, const int (&slot)[4], void* out,
+__device__ __forceinline__ void store_sum(Four<YBF16> (&y)[4], const int (&slot)[4], void* out,
                                           const size_t (&row)[4], int n, const v4f (&acc)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (!based) y[i] = {};
     y[i].add(v4f{acc[0][i], acc[1][i], acc[2][i], acc[3][i]}, slot[i] < 0);
     y[i].store_all(out, row[i] + n);
   }
@@ -612,19 +611,20 @@ __device__ __forceinline__ void store_sum(Four<YBF16> (&y)[4], bool based, const
 // unconditional, so the pieces of the next G steps (fetched as soon as the last
 // have gone to LDS) and the next block's base stay in flight meanwhile.
 // `ready` is called once the first loads are under way: v is there after it.
-template <bool YBF16, int G, bool ONCE, class Ready>
+// BASED: there is a base.
+template <bool YBF16, bool BASED, int G, bool ONCE, class Ready>
 __device__ __forceinline__ void blocks(Ready&& ready, const moe_lora& L, const Step* list, int steps,
                                        const int (&slot)[4], const size_t (&row)[4],
                                        const uint16_t (&vs)[kParts][16][kVStride], int nb, int n1, const void* base,
-                                       bool based, void* out, char* lds) {
+                                       void* out, char* lds) {
   const int n = (threadIdx.x & 15) * 4, r = L.r;
-  Four<YBF16> y[4], y_next[4];
+  Four<YBF16> y[4] = {}, y_next[4] = {};
   Pieces p[G];
   Step s[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) s[g] = fetch(list, ONCE ? g : min(g, steps - 1));
   if (nb < n1) {
-    load_base(y, base, row, nb + n);
+    if constexpr (BASED) load_base(y, base, row, nb + n);
 #pragma unroll
     for (int g = 0; g < G; ++g) p[g].load(s[g], nb, r);
   }
@@ -632,7 +632,7 @@ __device__ __forceinline__ void blocks(Ready&& ready, const moe_lora& L, const S
   for (; nb < n1; nb += kTileWaves * 64) {
     const int nb2 = nb + kTileWaves * 64 < n1 ? nb + kTileWaves * 64 : nb;
     v4f acc[4] = {}, d[4] = {};
-    load_base(y_next, base, row, nb2 + n);
+    if constexpr (BASED) load_base(y_next, base, row, nb2 + n);
     for (int u = 0; u < (ONCE ? G : steps); u += G) {
       const bool end = ONCE || u + G >= steps;
 #pragma unroll
@@ -652,7 +652,7 @@ __device__ __forceinline__ void blocks(Ready&& ready, const moe_lora& L, const S
         }
       }
     }
-    store_sum(y, based, slot, out, row, nb + n, acc);
+    store_sum(y, slot, out, row, nb + n, acc);
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = y_next[i];
   }
@@ -789,7 +789,6 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
   }
   const int n1 = min(N, n0 + per);
   int nb = n0 + wave * 64;
-  const bool based = base != nullptr;
   auto last = [&] {
     if (ntask > 0) join((ntask - 1) / kPass * kPass, (ntask - 1) % kPass + 1);
   };
@@ -797,10 +796,13 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
     // whole blocks (per is a multiple of 64); where r is not a multiple of eight the
     // last pieces run into the next seven rows, which have to be inside B
     const int whole = r % 8 == 0 ? n1 / 64 * 64 : max(0, min(n1, N - 7)) / 64 * 64;
-    const void* from = based ? base : out;
     auto run = [&](auto g, auto once) {
-      blocks<YBF16, decltype(g)::value, decltype(once)::value>(last, L, step, steps, slot, row, vs, nb, whole, from,
-                                                                   based, out, lds);
+      constexpr int G = decltype(g)::value;
+      constexpr bool ONCE = decltype(once)::value;
+      if (base)
+        blocks<YBF16, true, G, ONCE>(last, L, step, steps, slot, row, vs, nb, whole, base, out, lds);
+      else
+        blocks<YBF16, false, G, ONCE>(last, L, step, steps, slot, row, vs, nb, whole, base, out, lds);
     };
     using yes = std::true_type;
     if (steps == 1)
