@@ -194,7 +194,8 @@ moe_status moe_group_wide(const int32_t* keys, int n, int nkeys, int32_t* counts
  * squares passes fp32's range norms to 0, squares below it count as 0), one
  * rounding per output. */
 enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 };  /* none, [H], [T], [T][H] */
-enum { MOE_GATE_LINEAR = 0, MOE_GATE_SIGMOID = 1 };  /* the gate as it is, or 1 / (1 + exp(-gate)) */
+/* the gate as it is, or 1 / (1 + exp(-gate)): within 8 * 2^-24 of its value, 0 below 2^-126 */
+enum { MOE_GATE_LINEAR = 0, MOE_GATE_SIGMOID = 1 };
 
 typedef struct {
   int H;               /* 1..16384 */
