@@ -161,7 +161,8 @@ typedef struct {
 } moe_router;
 
 /*   logits [T][E] in lt (MOE_F32 or MOE_BF16), bias [E] fp32 or NULL,
- *   ids [T][k] int32 out, w [T][k] fp32 out.  0 <= T <= 2^20 (0: no launch). */
+ *   ids [T][k] int32 out, w [T][k] fp32 out, overlapping neither each other nor an
+ *   input.  0 <= T <= 2^20 (0: no launch). */
 moe_status moe_route_groups(const moe_router* router, const void* logits, moe_dtype lt, const float* bias, int T,
                             int32_t* ids, float* w, moe_stream_t stream);
 
@@ -211,7 +212,8 @@ typedef struct {
 } moe_norm;
 
 /* The norm before the block: out[t] = RMS(x[t]; pre_w).
- *   x [T][H] in xt, out [T][H] in ot; out may be x where xt == ot.
+ *   x [T][H] in xt, out [T][H] in ot; out may be x where xt == ot, and overlaps no
+ *   input otherwise.
  * 0 <= T <= 2^20 (0: no launch).  Pointers aligned to their element. */
 moe_status moe_norm_in(const moe_norm* norm, const void* x, moe_dtype xt, int T, void* out, moe_dtype ot,
                        moe_stream_t stream);
@@ -224,7 +226,8 @@ moe_status moe_norm_in(const moe_norm* norm, const void* x, moe_dtype xt, int T,
  *   y [T][H] in yt, residual and out [T][H] in rt, gate in gt (NULL with
  *   MOE_GATE_NONE), next_out [T][H] in nt; next and next_out both NULL: not
  *   computed.  next->H == norm->H.  out and next_out may each be the buffer of y
- *   or residual where the types are equal, and must differ from each other. */
+ *   or residual where the types are equal; they overlap no input otherwise, nor
+ *   each other. */
 moe_status moe_norm_out(const moe_norm* norm, const void* y, moe_dtype yt, const void* residual, const void* gate,
                         moe_dtype gt, int T, void* out, moe_dtype rt, const moe_norm* next, void* next_out,
                         moe_dtype nt, moe_stream_t stream);
@@ -249,8 +252,8 @@ typedef struct {
 } moe_lora;
 
 /*   x [T][K] in xt, adapter_ids [T] int32, base [T][N] in yt or NULL (zeros),
- *   out [T][N] in yt; out may be base.  0 <= T <= 2^20 (0: no launch).  a and b
- *   2-byte, the others element aligned (16-byte: wide loads). */
+ *   out [T][N] in yt; out may be base, and overlaps no input otherwise.
+ * 0 <= T <= 2^20 (0: no launch).  a and b 2-byte, the others element aligned. */
 moe_status moe_lora_add(const moe_lora* lora, const void* x, moe_dtype xt, int T, const int32_t* adapter_ids,
                         const void* base, void* out, moe_dtype yt, moe_stream_t stream);
 

@@ -376,6 +376,19 @@ constexpr int kMaxTokens = 1 << 20;  // rows of the calls below: a grid of 1024-
 bool is_dtype(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16; }
 size_t dsize(moe_dtype t) { return t == MOE_BF16 ? 2 : 4; }
 
+// A buffer of a call.  Workgroups write their rows while others still read theirs,
+// so an output may share memory with another buffer only row for row: the same one.
+struct Buffer {
+  const void* p;
+  size_t bytes;
+};
+
+bool overlap(Buffer a, Buffer b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+}
+bool overlap_part(Buffer a, Buffer b) { return a.p != b.p && overlap(a, b); }
+
 moe_status check_norm(const moe_norm* n, const char* who) {
   REQUIRE(n, MOE_EINVAL, "%s: norm is NULL", who);
   REQUIRE(n->H >= 1 && n->H <= 16384, MOE_ESHAPE, "%s: H=%d outside 1..16384", who, n->H);
@@ -421,6 +434,10 @@ moe_status moe_route_groups(const moe_router* R, const void* logits, moe_dtype l
   REQUIRE(logits && ids && w, MOE_EINVAL, "moe_route_groups: NULL pointer");
   REQUIRE(aligned(logits, dsize(lt)) && aligned(bias, 4) && aligned(ids, 4) && aligned(w, 4), MOE_EINVAL,
           "moe_route_groups: pointers must be aligned to their element");
+  const Buffer in{logits, (size_t)T * R->E * dsize(lt)}, b{bias, (size_t)R->E * 4};
+  const Buffer oi{ids, (size_t)T * R->k * 4}, ow{w, (size_t)T * R->k * 4};
+  REQUIRE(!overlap(oi, ow) && !overlap(oi, in) && !overlap(ow, in) && !overlap(oi, b) && !overlap(ow, b), MOE_EINVAL,
+          "moe_route_groups: ids and w may overlap neither each other nor an input");
   return launch_route_groups(R, logits, lt, bias, T, ids, w, (hipStream_t)stream);
 }
 
@@ -435,6 +452,10 @@ moe_status moe_norm_in(const moe_norm* norm, const void* x, moe_dtype xt, int T,
   REQUIRE(aligned(x, dsize(xt)) && aligned(out, dsize(ot)), MOE_EINVAL,
           "moe_norm_in: pointers must be aligned to their element");
   REQUIRE(x != out || xt == ot, MOE_EINVAL, "moe_norm_in: out may be x only where their types are equal");
+  const size_t n = (size_t)T * norm->H;
+  const Buffer o{out, n * dsize(ot)};
+  REQUIRE(!overlap_part(o, {x, n * dsize(xt)}) && !overlap(o, {norm->pre_w, norm->H * dsize(norm->wt)}), MOE_EINVAL,
+          "moe_norm_in: out may be x, but overlap no input otherwise");
   return launch_norm_in(norm, x, xt, T, out, ot, (hipStream_t)stream);
 }
 
@@ -462,6 +483,15 @@ moe_status moe_norm_out(const moe_norm* norm, const void* y, moe_dtype yt, const
   REQUIRE((out != y || yt == rt) && (!next || ((next_out != y || yt == nt) && (next_out != residual || rt == nt))),
           MOE_EINVAL, "moe_norm_out: an output may be an input's buffer only where their types are equal");
   REQUIRE(!gate || (gate != out && gate != next_out), MOE_EINVAL, "moe_norm_out: gate may not be an output's buffer");
+  const size_t n = (size_t)T * norm->H;
+  const size_t gates = norm->gate == MOE_GATE_CHANNEL ? norm->H : norm->gate == MOE_GATE_TOKEN ? T : n;
+  const Buffer outs[2] = {{out, n * dsize(rt)}, {next_out, n * dsize(nt)}};
+  for (const Buffer& o : outs)
+    REQUIRE(!overlap_part(o, {y, n * dsize(yt)}) && !overlap_part(o, {residual, n * dsize(rt)}) &&
+                !overlap(o, {gate, gates * dsize(gt)}) && !overlap(o, {norm->post_w, norm->H * dsize(norm->wt)}) &&
+                (!next || !overlap(o, {next->pre_w, norm->H * dsize(next->wt)})),
+            MOE_EINVAL, "moe_norm_out: an output may be y's or residual's buffer, but overlap no input otherwise");
+  REQUIRE(!overlap(outs[0], outs[1]), MOE_EINVAL, "moe_norm_out: out and next_out overlap");
   return launch_norm_out(norm, y, yt, residual, gate, gt, T, out, rt, next, next_out, nt, (hipStream_t)stream);
 }
 
@@ -482,6 +512,12 @@ moe_status moe_lora_add(const moe_lora* L, const void* x, moe_dtype xt, int T, c
   REQUIRE(aligned(x, dsize(xt)) && aligned(adapter_ids, 4) && aligned(base, dsize(yt)) && aligned(out, dsize(yt)),
           MOE_EINVAL, "moe_lora_add: pointers must be aligned to their element");
   REQUIRE(x != out, MOE_EINVAL, "moe_lora_add: out may not be x");
+  const size_t N = (size_t)L->N, K = (size_t)L->K, r = (size_t)L->r, num = (size_t)L->num;
+  const Buffer o{out, T * N * dsize(yt)};
+  REQUIRE(!overlap_part(o, {base, T * N * dsize(yt)}) && !overlap(o, {x, T * K * dsize(xt)}) &&
+              !overlap(o, {adapter_ids, (size_t)T * 4}) && !overlap(o, {L->a, num * r * K * 2}) &&
+              !overlap(o, {L->b, num * N * r * 2}) && !overlap(o, {L->scale, num * 4}) && !overlap(o, {L->ranks, num * 4}),
+          MOE_EINVAL, "moe_lora_add: out may be base, but overlap no input otherwise");
   return launch_lora(L, x, xt, T, adapter_ids, base, out, yt, (hipStream_t)stream);
 }
 
