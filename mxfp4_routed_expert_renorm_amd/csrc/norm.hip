@@ -195,10 +195,18 @@ constexpr int kCUs = 256;
 // streaming stores) above, where bandwidth does.  H = 4096, with one and two:
 // norm_in 1 row 2.2 and 2.4 us, 256 rows 2.7 and 2.8, 512 rows 3.15 and 3.05, 1024
 // rows 4.7 and 3.7, 4096 rows 14.1 and 12.0; norm_out 1 row 3.1 and 4.0, 256 rows 3.9
-// and 4.7, 512 rows 5.2 and 5.0, 1024 rows 9.3 and 8.1, 4096 rows 31.4 and 24.4.
+// and 4.7, 512 rows 5.2 and 5.0, 1024 rows 9.3 and 8.1, 4096 rows 31.4 and 24.4.  The
+// same from H = 520 to 8192: at 2^22 elements two gain 22 to 42% (norm_in) and 7 to 23%.
+// Rows of at most 64 chunks have no second one for their 64 threads: 16384 x 256
+// norm_in 6.8 and 8.1, norm_out 11.9 and 15.5; 8192 x 512 4.75 and 4.95, 9.3 and 9.6.
+// From 2^23 elements on the rows' loop, which comes with two, outweighs that for
+// norm_out where most of the 64 have one: 32768 x 512 31.1 and 24.6, 43691 x 384 36.0
+// and 32.2, but 52429 x 320 39.1 and 38.8, 65536 x 256 41.7 and 46.2.
 Shape shape(NormArgs& a, bool may_loop) {
   const int chunks = (a.H + 7) / 8;
-  const int v = chunks > 1024 || (size_t)a.T * a.H > (size_t)1 << 20 ? 2 : 1;
+  const size_t n = (size_t)a.T * a.H;
+  const bool two = chunks > 1024 || (chunks > 64 ? n > (size_t)1 << 20 : may_loop && chunks > 40 && n > (size_t)1 << 23);
+  const int v = two ? 2 : 1;
   int per = 64;
   while (per * v < chunks) per *= 2;
   const int block = max(per, 256), rows = block / per;
