@@ -233,11 +233,13 @@ moe_status moe_norm_out(const moe_norm* norm, const void* y, moe_dtype yt, const
                         moe_dtype nt, moe_stream_t stream);
 
 /* Low-rank adapters of many requests beside a projection that all of them
- * share (FP4 weights cannot take an adapter in without being quantised again):
+ * share: the router's, or the block as a whole.  (The experts' own projections run
+ * inside the fused expert calls, which this call does not reach.)
  *     out[t] = base[t] + scale[a] * B[a] (A[a] x[t]),   a = adapter_ids[t]
  * Only the first min(ranks[a], r) rows of A[a] and columns of B[a] count.  A
- * token whose id is outside [0, num) has no adapter: out[t] = base[t].  No
- * token's result depends on another's adapter.  fp32 sums, one rounding.
+ * token whose id is outside [0, num) or whose adapter's rank is 0 or less has no
+ * adapter: out[t] = base[t], bit for bit.  No token's result depends on another's
+ * adapter.  fp32 sums, one rounding.
  * Infinities in an adapter reach its tokens as infinities or NaN.
  * Requests' tokens may stand in any order; long batches run best where a
  * request's tokens stand together. */

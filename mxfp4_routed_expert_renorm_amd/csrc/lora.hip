@@ -34,11 +34,14 @@ __device__ __forceinline__ int rank_of(const moe_lora& L, int id) {
 // at a stride of 512, S such steps in flight.  B v: LANES lanes share a row of B,
 // each with its eight ranks of v in registers, so that a wavefront's loads are
 // contiguous.  The first rows of B and the base do not depend on A x and are
-// requested before it: what is left is a chain of the id, the adapter's rank, A
-// and the reductions.  That chain bounds small calls (K = N = 4096, rank 16, one
-// token: 4.3 us, of which 1.9 are a launch); larger ranks are bound by what one
-// compute unit draws (rank 64, 64 tokens of 64 adapters: 16.8 us, 67 MB, 4.0 TB/s;
-// with ranks 8 to 64 mixed the tokens of rank 64 set the pace: 17.1 us).
+// requested before it: what is left is a chain of the id, the adapter's rank where
+// the bank has ranks, A and the reductions.  That chain bounds small calls (K = N =
+// 4096, rank 16, one token: 4.3 us, of which 1.9 are a launch; A comes in two bursts
+// of 2048 positions, the second requested after the first).  At rank 64, 64 tokens
+// of 64 adapters take 17.1 us for 67 MB, 3.9 TB/s: a token's four workgroups draw all
+// of its A each, 0.66 MB a workgroup with x and B, and wait for a group of rows whole
+// before they request the next.  With ranks 8 to 64 mixed, half the bytes, the tokens
+// of rank 64 set the pace: 17.0 us.
 
 constexpr int kTokThreads = 512, kTokWaves = kTokThreads / 64;
 constexpr int kTokOut = 1024;  // outputs gathered in LDS before they are written
@@ -258,9 +261,9 @@ __global__ __launch_bounds__(kTokThreads, WIDE ? 2 : 4) void token_kernel(moe_lo
 // so one adapter's NaN cannot reach another's tokens.
 //
 // Large calls are bound by memory: 4096 tokens, K = N = 4096, rank 32, bf16, one
-// request: 23.4 us, 4.3 TB/s over x, base, out and the adapter (5.1 is a copy's
+// request: 23.1 us, 4.4 TB/s over x, base, out and the adapter (5.2 is a copy's
 // rate).  A tile at the border of two requests takes longer than the others, and
-// at 4096 tokens every compute unit has one tile: twelve requests 29.7 us.
+// at 4096 tokens every compute unit has one tile: twelve requests 30.0 us.
 
 constexpr int kTileWaves = 8, kTileThreads = 64 * kTileWaves;
 constexpr int kMaxPass = 8;             // most tasks per pass over x
@@ -850,9 +853,9 @@ __global__ __launch_bounds__(kTileThreads) void tile_kernel(moe_lora L, const vo
 // (two tokens on one up to rank 16) for a chain of reads; the tile form once a
 // tile and distinct adapter, but takes 8 us for a tile at least.  Both measured
 // over 150 drawn calls (K, N 64..4096, r 1..64, up to 64 requests): this rule is
-// 1.0% off the better of the two on the mean, the token form alone 23%, the tile
-// form alone 102%.  E.g. K = N = 4096, r = 16, bf16: 128 tokens 8.5 against 11.8 us,
-// 1024 tokens 41.6 against 15.7.
+// 1.0% off the better of the two on the mean (62% at most, where both take under 15
+// us), the token form alone 23%, the tile form alone 101%.  E.g. K = N = 4096, r = 16,
+// bf16, twelve requests: 128 tokens 8.6 against 14.9 us, 1024 tokens 24.9 against 15.6.
 bool token_form(const moe_lora* L, int T) {
   const double products = (double)T * L->r * ((double)L->K + L->N);
   return T <= 128 || (products <= 24e6 && (T <= 512 || (L->r <= 16 && T <= 1536)));

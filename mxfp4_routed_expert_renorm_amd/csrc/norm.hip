@@ -10,11 +10,12 @@
 // row needs (weights and gate too) is requested before the first sum is formed.
 // Sums and everything between are fp32; each output is rounded once.
 //
-// Bound by memory: 4096 x 4096 bf16, norm_in 12.0 us (67 MB, 5.6 TB/s; a copy
-// reaches 5.1), norm_out with a channel gate and the next norm 24.4 us (134 MB,
-// 5.5 TB/s).  Large results are stored streaming: with ordinary stores the lines
+// Bound by memory: 4096 x 4096 bf16, norm_in 12.1 us (67 MB, 5.5 TB/s; a copy of
+// as many bytes, which stays in the Infinity Cache from call to call, takes 10.6),
+// norm_out with a channel gate and the next norm 24.3 us (134 MB, 5.5 TB/s; a copy
+// 26.7).  Large results are stored streaming: with ordinary stores the lines
 // left dirty in the L2s are written back at the kernel's end, 13.3 and 28.2 us.
-// Rows of odd width pay for stores that share lines: 509 x 2047 6.2 us, 509 x 2048
+// Rows of odd width pay for stores that share lines: 509 x 2047 6.3 us, 509 x 2048
 // 4.5.  One row: 2.2 and 3.1 us, of which 1.9 are a launch.
 #include "chunk_dev.h"
 
