@@ -259,6 +259,114 @@ typedef struct {
 moe_status moe_lora_add(const moe_lora* lora, const void* x, moe_dtype xt, int T, const int32_t* adapter_ids,
                         const void* base, void* out, moe_dtype yt, moe_stream_t stream);
 
+/* ------------------------------------------------------------ to the experts and back */
+
+/* The (token, rank) pairs sorted by expert, and the tokens' rows copied into that
+ * order, so that each expert's rows stand together (moe_q4_grouped reads them so).
+ * Pair p = t * k + r of token t has expert ids[t][r]; an id outside [0, E) drops the
+ * pair.  The sort is stable: an expert's pairs keep their order.
+ *   offsets[e]  sorted rows of expert e: [offsets[e], offsets[e + 1]); offsets[E] = live pairs
+ *   perm[i]     the pair at sorted row i < offsets[E]
+ *   rows[t][r]  the sorted row of the pair, -1 if it is dropped
+ *   xs[i]       x[perm[i] / k]
+ * Entries of perm and rows of xs from offsets[E] on are left as they were.
+ *   x [T][H] in xt, xs [T*k][H] in xt, both NULL: the indices alone (H is then not
+ *   used); ids [T][k], offsets [E + 1], perm [T*k], rows [T][k] int32.
+ * 0 <= T, 1 <= k <= 64, T*k <= 2^20, 1 <= E <= 1024, 1 <= H <= 65536; pointers
+ * aligned to their element; no output overlaps an input or another output.
+ * scratch: device, 4-byte aligned, at least moe_permute_scratch_bytes(T, k, E) bytes,
+ * rewritten by every call (calls that may run at the same time need scratch of their
+ * own); NULL where that is 0. */
+size_t moe_permute_scratch_bytes(int T, int k, int E);
+moe_status moe_permute(const void* x, moe_dtype xt, int T, int k, int H, int E, const int32_t* ids, void* xs,
+                       int32_t* offsets, int32_t* perm, int32_t* rows, void* scratch, size_t scratch_bytes,
+                       moe_stream_t stream);
+
+/* The way back, with the weights applied:
+ *     out[t] = sum over r of w[t][r] * ys[rows[t][r]]  (+ base[t])
+ * A pair whose row is outside [0, M) is dropped; a dropped pair's weight and no row
+ * of ys but the pairs' own reach the sum.  fp32 in rank order, base last, one
+ * rounding.  w NULL: weights of 1, which is the gradient of moe_permute (ys the
+ * gradient of xs, out that of x).
+ *   ys [M][H] in yt, rows [T][k] int32, w [T][k] fp32 or NULL, base [T][H] in ot or
+ *   NULL, out [T][H] in ot; out may be base, and overlaps no input otherwise.
+ * 0 <= T <= 2^20, 0 <= M <= 2^20, 1 <= k <= 64, 1 <= H <= 65536. */
+moe_status moe_unpermute(const void* ys, moe_dtype yt, int M, const int32_t* rows, const float* w, const void* base,
+                         int T, int k, int H, void* out, moe_dtype ot, moe_stream_t stream);
+
+/* The gradient of moe_unpermute (that of base is gout itself):
+ *     gys[rows[t][r]] = w[t][r] * gout[t],     gw[t][r] = sum over h of gout[t][h] * ys[rows[t][r]][h]
+ * Dropped pairs have gw 0 and no row; rows of gys that no pair has are left as they
+ * were.  Rows are moe_permute's: no two pairs share one (of two that do, one's gys
+ * stays).  fp32 sums, one rounding.
+ *   gout [T][H] in gt, ys [M][H] in yt (NULL where gw is), rows [T][k], w [T][k] fp32
+ *   or NULL (1), gys [M][H] in yt or NULL (not computed), gw [T][k] fp32 or NULL (not
+ *   computed).  gys may be ys; no output overlaps an input or the other otherwise.
+ * Sizes as moe_unpermute. */
+moe_status moe_unpermute_grad(const void* gout, moe_dtype gt, const void* ys, moe_dtype yt, int M, const int32_t* rows,
+                              const float* w, int T, int k, int H, void* gys, float* gw, moe_stream_t stream);
+
+/* The gradient of moe_route_groups' weights with respect to the logits, the picks
+ * being fixed (the bias and the groups steer the choice and have none).  With
+ * s = softmax or sigmoid scores and m = sum g w / sum w over the token's picks if
+ * router->renorm, else 0:
+ *     sigmoid            d[pick] = w (1 - s[pick]) (g - m)
+ *     softmax, renorm    d[pick] = w (g - m)
+ *     softmax            d[e]    = sum over picks of e of g w - s[e] * sum over picks of g w,  every e
+ * and 0 for all other experts.  A pick of weight 0 (masked) or outside [0, E) adds
+ * nothing, whatever its g; an expert picked twice gets the sum.  Masked logits (as
+ * moe_route_groups') have s = 0.
+ *   logits [T][E] in lt, ids [T][k] and w [T][k] as moe_route_groups gave them (or
+ *   moe_route: softmax, renorm), gw [T][k] fp32: the loss's gradient of w,
+ *   glogits [T][E] in gt: every element written; overlaps no input.
+ * 0 <= T <= 2^20. */
+moe_status moe_route_grad(const moe_router* router, const void* logits, moe_dtype lt, int T, const int32_t* ids,
+                          const float* w, const float* gw, void* glogits, moe_dtype gt, moe_stream_t stream);
+
+/* ------------------------------------------------------------ products with 4-bit weights */
+
+/* Matrices of 4-bit codes with a scale for each group of inputs: a projection beside
+ * the experts (num = 1), or the experts' own.
+ *     W[n][i] = scale[n][i / group] * v(code[n][i]),   y[t][n] = sum over i of W[n][i] x[t][i]
+ *   MOE_Q4_INT4: v = code - zero[n][i / group], codes 0..15, zeros NULL: 8
+ *   MOE_Q4_FP4:  v = the E2M1 value (sign, 2-bit exponent, mantissa), as the expert records'
+ *   MOE_Q4_LINEAR: y as above;  MOE_Q4_SWIGLU: the matrix has 2 N rows, gate above up,
+ *   and y[t][n] = silu(gate) * up
+ * Two codes per byte, input 2j in the low nibble.  A group's sum of v * x is formed in
+ * fp32 from exact products (fp32 x keeps all its bits), then scaled and added in fp32;
+ * y is rounded once.  An infinity or NaN in a row of x leaves that row of y infinite or
+ * NaN, and no other row.
+ * An expert record (see above) holds two such matrices: w1 and w3 with their scales
+ * stand together as a SWIGLU matrix of I outputs, w2 as a LINEAR one of H. */
+enum { MOE_Q4_INT4 = 0, MOE_Q4_FP4 = 1 };
+enum { MOE_Q4_LINEAR = 0, MOE_Q4_SWIGLU = 1 };
+enum { MOE_SCALE_E8M0 = 2 }; /* beside MOE_F32 and MOE_BF16: a byte e, 2^(e - 127) */
+
+typedef struct {
+  int K, N;             /* inputs, a multiple of 32, and outputs: 1..65536 */
+  int num;              /* matrices, 1..1024 */
+  int group;            /* inputs per scale: a multiple of 32 that divides K */
+  int code;             /* MOE_Q4_INT4 or MOE_Q4_FP4 */
+  int act;              /* MOE_Q4_LINEAR or MOE_Q4_SWIGLU */
+  int32_t st;           /* type of the scales: MOE_F32, MOE_BF16 or MOE_SCALE_E8M0 */
+  const uint8_t* codes; /* [num][R][K/2], R = N or 2 N; 16-byte aligned */
+  const void* scales;   /* [num][R][K/group] */
+  const uint8_t* zeros; /* [num][R][K/group], one byte 0..15 each, or NULL; INT4 alone */
+  size_t code_stride, scale_stride, zero_stride; /* bytes between matrices; code_stride a multiple of 16 */
+} moe_q4;
+
+/* y[t] = W[0] x[t]: x [T][K] in xt, y [T][N] in yt, overlapping no input.
+ * 0 <= T <= 2^20.  Pointers aligned to their element. */
+moe_status moe_q4_linear(const moe_q4* q, const void* x, moe_dtype xt, int T, void* y, moe_dtype yt,
+                         moe_stream_t stream);
+
+/* Rows sorted by matrix: y[i] = W[e] x[i] for i in [offsets[e], offsets[e + 1]).
+ * offsets [num + 1] int32 (moe_permute's): rising, from 0 on, at most P; anything else
+ * leaves some rows of y undefined.  Rows of y outside every range are left as they were.
+ *   x [P][K] in xt, y [P][N] in yt, overlapping no input.  0 <= P <= 2^20. */
+moe_status moe_q4_grouped(const moe_q4* q, const void* x, moe_dtype xt, int P, const int32_t* offsets, void* y,
+                          moe_dtype yt, moe_stream_t stream);
+
 /* ------------------------------------------------------------ expert MLP */
 
 /* Workspace bytes moe_expert_forward and moe_layer_decode need for T tokens,
@@ -587,6 +695,8 @@ typedef enum {
   MOE_PROF_SCRATCH = 14,    /* one-time clear of the static scratch (moe_layer_decode_noalloc) */
   MOE_PROF_NORM = 15,       /* norms around the block */
   MOE_PROF_LORA = 16,       /* requests' adapters */
+  MOE_PROF_PERMUTE = 17,    /* rows to the experts' order and back, and the gradients */
+  MOE_PROF_Q4 = 18,         /* products with 4-bit weights */
   MOE_PROF_KINDS = 24
 } moe_prof_kind;
 

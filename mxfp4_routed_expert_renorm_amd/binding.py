@@ -92,6 +92,20 @@ class moe_lora(ctypes.Structure):
     ]
 
 
+Q4_INT4, Q4_FP4 = 0, 1
+Q4_LINEAR, Q4_SWIGLU = 0, 1
+SCALE_E8M0 = 2
+
+
+class moe_q4(ctypes.Structure):
+    _dev, _tensors = None, ()  # device of the tensors it keeps, and these
+    _fields_ = [
+        ("K", c_int), ("N", c_int), ("num", c_int), ("group", c_int), ("code", c_int), ("act", c_int), ("st", c_int),
+        ("codes", c_void_p), ("scales", c_void_p), ("zeros", c_void_p),
+        ("code_stride", c_size_t), ("scale_stride", c_size_t), ("zero_stride", c_size_t),
+    ]
+
+
 _SIGS = {
     "moe_last_error": (c_char_p, []),
     "moe_version": (c_char_p, []),
@@ -104,6 +118,17 @@ _SIGS = {
     "moe_norm_out": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_int, c_int, c_void_p, c_int, c_void_p,
                              c_void_p, c_int, c_void_p]),
     "moe_lora_add": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_int, c_void_p]),
+    "moe_permute_scratch_bytes": (c_size_t, [c_int, c_int, c_int]),
+    "moe_permute": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+                            c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_unpermute": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_void_p,
+                              c_int, c_void_p]),
+    "moe_unpermute_grad": (c_int, [c_void_p, c_int, c_void_p, c_int, c_int, c_void_p, c_void_p, c_int, c_int, c_int,
+                                   c_void_p, c_void_p, c_void_p]),
+    "moe_route_grad": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+                               c_void_p]),
+    "moe_q4_linear": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_int, c_void_p]),
+    "moe_q4_grouped": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p, c_int, c_void_p]),
     "moe_group": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p]),
     "moe_group_scratch_bytes": (c_size_t, [c_int, c_int]),
     "moe_group_wide": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
@@ -476,6 +501,198 @@ def moe_lora_add(lora: moe_lora, x, adapter_ids, base, out, stream=None):
     return out
 
 
+# ------------------------------------------------------- to the experts and back
+
+def moe_permute_scratch_bytes(T, k, E) -> int:
+    return load().moe_permute_scratch_bytes(T, k, E)
+
+
+def moe_permute(x, ids, xs, offsets, perm, rows, scratch=None, stream=None):
+    """(token, rank) pairs of ids [T, k] int32 sorted by expert: offsets [E + 1], perm
+    [T * k] and rows [T, k] int32 (-1: dropped), xs [T * k, H] = x [T, H] in that order (x
+    and xs None: the indices alone).  scratch: a tensor of moe_permute_scratch_bytes bytes
+    on the device, None where that is 0."""
+    types, shape, dev = _type_codes or _types(), ids.shape, ids.get_device()
+    torch, (T, k), E = _torch_module, shape if len(shape) == 2 else (-1, -1), offsets.numel() - 1
+    i32, H, xt, xp, xsp = torch.int32, 0, 0, None, None
+    good = (ids.dtype is i32 and offsets.dtype is i32 and perm.dtype is i32 and rows.dtype is i32
+            and T >= 0 and rows.shape == shape and perm.shape == (T * k,) and offsets.dim() == 1
+            and dev >= 0 and dev == _device_now() and dev == offsets.get_device() and dev == perm.get_device()
+            and dev == rows.get_device() and ids.is_contiguous() and offsets.is_contiguous()
+            and perm.is_contiguous() and rows.is_contiguous()
+            and (scratch is None or (dev == scratch.get_device() and scratch.is_contiguous())))
+    if (x is None) != (xs is None):
+        raise ValueError("moe_permute: x and xs must both be given or both be None")
+    if x is not None:
+        xt, H, xp, xsp = types.get(x.dtype), x.shape[-1], x.data_ptr(), xs.data_ptr()
+        good = (good and xt is not None and xs.dtype is x.dtype and x.shape == (T, H) and xs.shape == (T * k, H)
+                and dev == x.get_device() and dev == xs.get_device() and x.is_contiguous() and xs.is_contiguous())
+    if not good:
+        if T < 0 or offsets.dim() != 1:
+            raise ValueError("moe_permute: ids is [T, k] and offsets [E + 1]")
+        _refuse("moe_permute", (), (("ids", ids, (T, k), (i32,)), ("offsets", offsets, (E + 1,), (i32,)),
+                                    ("perm", perm, (T * k,), (i32,)), ("rows", rows, (T, k), (i32,)),
+                                    ("x", x, (T, H), types), ("xs", xs, (T * k, H), () if x is None else (x.dtype,)),
+                                    ("scratch", scratch, () if scratch is None else scratch.shape,
+                                     () if scratch is None else (scratch.dtype,))))
+    st = load().moe_permute(xp, xt, T, k, H, E, ids.data_ptr(), xsp, offsets.data_ptr(), perm.data_ptr(),
+                            rows.data_ptr(), None if scratch is None else scratch.data_ptr(),
+                            0 if scratch is None else scratch.numel() * scratch.element_size(),
+                            _stream_now(dev) if stream is None else _stream(stream))
+    if st:
+        _check("moe_permute", st)
+    return xs
+
+
+def moe_unpermute(ys, rows, w, base, out, stream=None):
+    """out [T, H] = base [T, H] (or zeros) + the rows rows [T, k] of ys [M, H], weighted by
+    w [T, k] float32 (None: 1).  Without w it is moe_permute's gradient."""
+    types, shape, dev = _type_codes or _types(), rows.shape, out.get_device()
+    torch, (T, k), (M, H) = _torch_module, shape if len(shape) == 2 else (-1, -1), ys.shape
+    yt, ot, outs = types.get(ys.dtype), types.get(out.dtype), out.shape
+    if not (yt is not None and ot is not None and rows.dtype is torch.int32 and outs == (T, H)
+            and dev >= 0 and dev == _device_now() and dev == ys.get_device() and dev == rows.get_device()
+            and ys.is_contiguous() and rows.is_contiguous() and out.is_contiguous()
+            and (w is None or (w.dtype is torch.float32 and w.shape == shape and w.is_contiguous()
+                               and dev == w.get_device()))
+            and (base is None or base is out or (base.dtype is out.dtype and base.shape == outs and base.is_contiguous()
+                                                 and dev == base.get_device()))):
+        _refuse("moe_unpermute", (), (("out", out, (T, H), types), ("ys", ys, (M, H), types),
+                                      ("rows", rows, (T, k), (torch.int32,)), ("w", w, (T, k), (torch.float32,)),
+                                      ("base", base, (T, H), (out.dtype,))))
+    st = load().moe_unpermute(ys.data_ptr(), yt, M, rows.data_ptr(), None if w is None else w.data_ptr(),
+                              None if base is None else base.data_ptr(), T, k, H, out.data_ptr(), ot,
+                              _stream_now(dev) if stream is None else _stream(stream))
+    if st:
+        _check("moe_unpermute", st)
+    return out
+
+
+def moe_unpermute_grad(gout, ys, rows, w, gys, gw, stream=None):
+    """The gradient of moe_unpermute: gout [T, H] -> gys [M, H] (the rows' gradients; None:
+    not computed) and gw [T, k] float32 (the weights'; None: not computed, and ys may be None)."""
+    types, shape, dev = _type_codes or _types(), rows.shape, gout.get_device()
+    torch, (T, k), H, some = _torch_module, shape if len(shape) == 2 else (-1, -1), gout.shape[-1], gys
+    if gys is None:
+        some = ys
+    if some is None or (gw is not None and ys is None):
+        raise ValueError("moe_unpermute_grad: gw needs ys, and without gw there must be gys")
+    M, gt, yt = some.shape[0], types.get(gout.dtype), types.get(some.dtype)
+    if not (gt is not None and yt is not None and rows.dtype is torch.int32 and gout.shape == (T, H)
+            and some.shape == (M, H) and dev >= 0 and dev == _device_now() and dev == some.get_device()
+            and dev == rows.get_device() and gout.is_contiguous() and rows.is_contiguous() and some.is_contiguous()
+            and (ys is None or ys is some or (ys.dtype is some.dtype and ys.shape == some.shape and ys.is_contiguous()
+                                              and dev == ys.get_device()))
+            and (w is None or (w.dtype is torch.float32 and w.shape == shape and w.is_contiguous()
+                               and dev == w.get_device()))
+            and (gw is None or (gw.dtype is torch.float32 and gw.shape == shape and gw.is_contiguous()
+                                and dev == gw.get_device()))):
+        _refuse("moe_unpermute_grad", (),
+                (("gout", gout, (T, H), types), ("rows", rows, (T, k), (torch.int32,)), ("gys", gys, (M, H), types),
+                 ("ys", ys, (M, H), types if gys is None else (gys.dtype,)), ("w", w, (T, k), (torch.float32,)),
+                 ("gw", gw, (T, k), (torch.float32,))))
+    st = load().moe_unpermute_grad(gout.data_ptr(), gt, None if ys is None else ys.data_ptr(), yt, M, rows.data_ptr(),
+                                   None if w is None else w.data_ptr(), T, k, H,
+                                   None if gys is None else gys.data_ptr(), None if gw is None else gw.data_ptr(),
+                                   _stream_now(dev) if stream is None else _stream(stream))
+    if st:
+        _check("moe_unpermute_grad", st)
+    return gys, gw
+
+
+def moe_route_grad(router: moe_router, logits, ids, w, gw, glogits, stream=None):
+    """The gradient of moe_route_groups' weights: logits [T, E], the picks ids [T, k] int32
+    with their weights w [T, k] and gw [T, k] float32, the loss's gradient of w -> glogits
+    [T, E] (float32 or bfloat16)."""
+    types, shape, dev = _type_codes or _types(), logits.shape, logits.get_device()
+    T, E, k, torch, picks = shape[0], router.E, router.k, _torch_module, ids.shape
+    lt, gt = types.get(logits.dtype), types.get(glogits.dtype)
+    if not (lt is not None and gt is not None and shape == (T, E) and shape == glogits.shape
+            and picks == (T, k) and picks == w.shape and picks == gw.shape
+            and ids.dtype is torch.int32 and w.dtype is torch.float32 and gw.dtype is torch.float32
+            and dev >= 0 and dev == _device_now() and dev == ids.get_device() and dev == w.get_device()
+            and dev == gw.get_device() and dev == glogits.get_device() and logits.is_contiguous()
+            and ids.is_contiguous() and w.is_contiguous() and gw.is_contiguous() and glogits.is_contiguous()):
+        f32 = (torch.float32,)
+        _refuse("moe_route_grad", (), (("logits", logits, (T, E), types), ("ids", ids, (T, k), (torch.int32,)),
+                                       ("w", w, (T, k), f32), ("gw", gw, (T, k), f32),
+                                       ("glogits", glogits, (T, E), types)))
+    st = load().moe_route_grad(ctypes.addressof(router), logits.data_ptr(), lt, T, ids.data_ptr(), w.data_ptr(),
+                               gw.data_ptr(), glogits.data_ptr(), gt,
+                               _stream_now(dev) if stream is None else _stream(stream))
+    if st:
+        _check("moe_route_grad", st)
+    return glogits
+
+
+# --------------------------------------------------- products with 4-bit weights
+
+def make_q4(codes, scales, zeros=None, code="int4", act="none") -> moe_q4:
+    """Matrices of 4-bit codes: codes [num, R, K / 2] uint8 (two a byte, input 2j in the
+    low nibble), scales [num, R, K / group] float32, bfloat16 or uint8 (E8M0), zeros as
+    scales, uint8 (None: 8; "int4" alone); num may be left out.  code: "int4" or "fp4"
+    (E2M1).  act: "none", or "swiglu" (the upper half of the R rows is the gate, the lower
+    half what it multiplies).  The matrices are dense and may stand apart (codes' by a
+    multiple of 16 bytes).  Keeps references."""
+    import torch
+    ts = [t if t is None or t.dim() == 3 else t.unsqueeze(0) for t in (codes, scales, zeros)]
+    c, s, z = ts
+    if c.dim() != 3 or s.dim() != 3 or (z is not None and z.dim() != 3):
+        raise ValueError("make_q4: codes are [num, R, K / 2] and scales [num, R, K / group]")
+    num, R, half = c.shape
+    G = s.shape[2]
+    st = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.uint8: SCALE_E8M0}.get(s.dtype)
+    if c.dtype != torch.uint8 or st is None or (z is not None and z.dtype != torch.uint8):
+        raise TypeError(f"make_q4: codes are {c.dtype}, scales {s.dtype}, zeros {None if z is None else z.dtype}")
+    halves = 2 if act == "swiglu" else 1
+    if G < 1 or (2 * half) % G or R % halves or s.shape[:2] != c.shape[:2] or (z is not None and z.shape != s.shape):
+        raise ValueError(f"make_q4: codes {tuple(c.shape)}, scales {tuple(s.shape)}, "
+                         f"zeros {None if z is None else tuple(z.shape)} do not belong together")
+    for what, t in (("codes", c), ("scales", s), ("zeros", z)):
+        if t is not None and t.numel() and not t[0].is_contiguous():
+            raise ValueError(f"make_q4: each matrix of {what} must be dense (row-major, contiguous)")
+    far = [0 if t is None or num <= 1 else t.stride(0) * t.element_size() for t in (c, s, z)]
+    q = moe_q4(2 * half, R // halves, num, 2 * half // G, {"int4": Q4_INT4, "fp4": Q4_FP4}[code],
+               {"none": Q4_LINEAR, "swiglu": Q4_SWIGLU}[act], st, c.data_ptr(), s.data_ptr(),
+               None if z is None else z.data_ptr(), *far)
+    q._tensors = (c, s, z)
+    q._dev = _one_device("make_q4", q._tensors)
+    return q
+
+
+def moe_q4_linear(q4: moe_q4, x, y, stream=None):
+    """y [T, N] = W x [T, K] with the descriptor's first matrix."""
+    types, shape, dev = _type_codes or _types(), x.shape, x.get_device()
+    T, xt, yt = shape[0], types.get(x.dtype), types.get(y.dtype)
+    if not (xt is not None and yt is not None and shape == (T, q4.K) and y.shape == (T, q4.N)
+            and dev >= 0 and dev == _device_now() and dev == y.get_device() and dev == q4._dev
+            and x.is_contiguous() and y.is_contiguous()):
+        _refuse("moe_q4_linear", (q4,), (("x", x, (T, q4.K), types), ("y", y, (T, q4.N), types)))
+    st = load().moe_q4_linear(ctypes.addressof(q4), x.data_ptr(), xt, T, y.data_ptr(), yt,
+                              _stream_now(dev) if stream is None else _stream(stream))
+    if st:
+        _check("moe_q4_linear", st)
+    return y
+
+
+def moe_q4_grouped(q4: moe_q4, x, offsets, y, stream=None):
+    """y [P, N] = W[e] x [P, K] for the rows [offsets[e], offsets[e + 1]) of each matrix e
+    (offsets [num + 1] int32 on the device, as moe_permute gives them)."""
+    types, shape, dev = _type_codes or _types(), x.shape, x.get_device()
+    P, xt, yt = shape[0], types.get(x.dtype), types.get(y.dtype)
+    if not (xt is not None and yt is not None and shape == (P, q4.K) and y.shape == (P, q4.N)
+            and offsets.dtype is _torch_module.int32 and offsets.shape == (q4.num + 1,)
+            and dev >= 0 and dev == _device_now() and dev == y.get_device() and dev == q4._dev
+            and dev == offsets.get_device() and x.is_contiguous() and y.is_contiguous() and offsets.is_contiguous()):
+        _refuse("moe_q4_grouped", (q4,), (("x", x, (P, q4.K), types), ("y", y, (P, q4.N), types),
+                                          ("offsets", offsets, (q4.num + 1,), (_torch_module.int32,))))
+    st = load().moe_q4_grouped(ctypes.addressof(q4), x.data_ptr(), xt, P, offsets.data_ptr(), y.data_ptr(), yt,
+                               _stream_now(dev) if stream is None else _stream(stream))
+    if st:
+        _check("moe_q4_grouped", st)
+    return y
+
+
 # ----------------------------------------------------------------- expert MLP
 
 def make_layer(H, I, fp4_base=None, fp4_stride=0, num_slots=0, int2_base=None, int2_stride=0, num_int2=0,
@@ -704,7 +921,8 @@ class Cache:
 # --------------------------------------------------------------------- timing
 
 PROF_KINDS = ("route", "router_logits", "gateup", "down", "combine", "group", "plan", "quant",
-              "gemm_gateup", "gemm_down", "dequant", "read", "cache", "fused", "scratch", "norm", "lora")
+              "gemm_gateup", "gemm_down", "dequant", "read", "cache", "fused", "scratch", "norm", "lora",
+              "permute", "q4")
 MOE_PROF_KINDS = 24
 
 

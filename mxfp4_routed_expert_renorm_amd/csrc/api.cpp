@@ -81,6 +81,19 @@ moe_status launch_norm_out(const moe_norm* n, const void* y, moe_dtype yt, const
 moe_status launch_lora(const moe_lora* L, const void* x, moe_dtype xt, int T, const int32_t* ids, const void* base,
                        void* out, moe_dtype yt, hipStream_t s);
 
+size_t permute_scratch_bytes(int T, int k, int E);
+moe_status launch_permute(const void* x, moe_dtype xt, int T, int k, int H, int E, const int32_t* ids, void* xs,
+                          int32_t* offsets, int32_t* perm, int32_t* rows, int32_t* scratch, hipStream_t s);
+moe_status launch_unpermute(const void* ys, moe_dtype yt, int M, const int32_t* rows, const float* w, const void* base,
+                            int T, int k, int H, void* out, moe_dtype ot, hipStream_t s);
+moe_status launch_unpermute_grad(const void* gout, moe_dtype gt, const void* ys, moe_dtype yt, int M,
+                                 const int32_t* rows, const float* w, int T, int k, int H, void* gys, float* gw,
+                                 hipStream_t s);
+moe_status launch_route_grad(const moe_router* R, const void* logits, moe_dtype lt, int T, const int32_t* ids,
+                             const float* w, const float* gw, void* glogits, moe_dtype gt, hipStream_t s);
+moe_status launch_q4(const moe_q4* q, const void* x, moe_dtype xt, int T, const int32_t* offsets, void* y, moe_dtype yt,
+                     hipStream_t s);
+
 static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 static size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -405,29 +418,35 @@ moe_status check_norm(const moe_norm* n, const char* who) {
   return MOE_OK;
 }
 
+moe_status check_router(const moe_router* R, const char* who) {
+  REQUIRE(R, MOE_EINVAL, "%s: router is NULL", who);
+  REQUIRE(R->E >= 1 && R->E <= 1024, MOE_ESHAPE, "%s: E=%d outside 1..1024", who, R->E);
+  REQUIRE(R->k >= 1 && R->k <= R->E && R->k <= 64, MOE_EINVAL,
+          "%s: k=%d must satisfy 1 <= k <= min(E=%d, 64)", who, R->k, R->E);
+  REQUIRE(R->scoring == MOE_SCORE_SOFTMAX || R->scoring == MOE_SCORE_SIGMOID, MOE_EINVAL,
+          "%s: scoring=%d", who, R->scoring);
+  REQUIRE(R->groups >= 1 && R->groups <= 64 && R->E % R->groups == 0, MOE_EINVAL,
+          "%s: groups=%d must be 1..64 and divide E=%d", who, R->groups, R->E);
+  REQUIRE(R->topk_groups >= 1 && R->topk_groups <= R->groups, MOE_EINVAL,
+          "%s: topk_groups=%d outside 1..groups=%d", who, R->topk_groups, R->groups);
+  REQUIRE(R->topk_groups * (R->E / R->groups) >= R->k, MOE_EINVAL,
+          "%s: topk_groups=%d groups of %d experts hold fewer than k=%d", who, R->topk_groups,
+          R->E / R->groups, R->k);
+  REQUIRE(R->group_score == MOE_GROUP_MAX || R->group_score == MOE_GROUP_TOP2, MOE_EINVAL,
+          "%s: group_score=%d", who, R->group_score);
+  REQUIRE(R->renorm == 0 || R->renorm == 1, MOE_EINVAL, "%s: renorm=%d", who, R->renorm);
+  REQUIRE(std::isfinite(R->scale), MOE_EINVAL, "%s: scale must be finite", who);
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
 
 moe_status moe_route_groups(const moe_router* R, const void* logits, moe_dtype lt, const float* bias, int T,
                             int32_t* ids, float* w, moe_stream_t stream) {
-  REQUIRE(R, MOE_EINVAL, "moe_route_groups: router is NULL");
-  REQUIRE(R->E >= 1 && R->E <= 1024, MOE_ESHAPE, "moe_route_groups: E=%d outside 1..1024", R->E);
-  REQUIRE(R->k >= 1 && R->k <= R->E && R->k <= 64, MOE_EINVAL,
-          "moe_route_groups: k=%d must satisfy 1 <= k <= min(E=%d, 64)", R->k, R->E);
-  REQUIRE(R->scoring == MOE_SCORE_SOFTMAX || R->scoring == MOE_SCORE_SIGMOID, MOE_EINVAL,
-          "moe_route_groups: scoring=%d", R->scoring);
-  REQUIRE(R->groups >= 1 && R->groups <= 64 && R->E % R->groups == 0, MOE_EINVAL,
-          "moe_route_groups: groups=%d must be 1..64 and divide E=%d", R->groups, R->E);
-  REQUIRE(R->topk_groups >= 1 && R->topk_groups <= R->groups, MOE_EINVAL,
-          "moe_route_groups: topk_groups=%d outside 1..groups=%d", R->topk_groups, R->groups);
-  REQUIRE(R->topk_groups * (R->E / R->groups) >= R->k, MOE_EINVAL,
-          "moe_route_groups: topk_groups=%d groups of %d experts hold fewer than k=%d", R->topk_groups,
-          R->E / R->groups, R->k);
-  REQUIRE(R->group_score == MOE_GROUP_MAX || R->group_score == MOE_GROUP_TOP2, MOE_EINVAL,
-          "moe_route_groups: group_score=%d", R->group_score);
-  REQUIRE(R->renorm == 0 || R->renorm == 1, MOE_EINVAL, "moe_route_groups: renorm=%d", R->renorm);
-  REQUIRE(std::isfinite(R->scale), MOE_EINVAL, "moe_route_groups: scale must be finite");
+  const moe_status st = check_router(R, "moe_route_groups");
+  if (st != MOE_OK) return st;
   REQUIRE(is_dtype(lt), MOE_EINVAL, "moe_route_groups: bad dtype %d", (int)lt);
   REQUIRE(T >= 0 && T <= kMaxTokens, MOE_ESHAPE, "moe_route_groups: T=%d outside 0..2^20", T);
   if (T == 0) return MOE_OK;
@@ -519,6 +538,180 @@ moe_status moe_lora_add(const moe_lora* L, const void* x, moe_dtype xt, int T, c
               !overlap(o, {L->b, num * N * r * 2}) && !overlap(o, {L->scale, num * 4}) && !overlap(o, {L->ranks, num * 4}),
           MOE_EINVAL, "moe_lora_add: out may be base, but overlap no input otherwise");
   return launch_lora(L, x, xt, T, adapter_ids, base, out, yt, (hipStream_t)stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ to the experts and back
+
+namespace {
+
+constexpr int kMaxPairs = 1 << 20;  // pairs of a sort, as moe_group's keys, and sorted rows
+constexpr int kMaxWidth = 65536;
+
+// the sizes of moe_unpermute and its gradient
+moe_status check_rows(int T, int k, int H, int M, const char* who) {
+  REQUIRE(T >= 0 && T <= kMaxTokens, MOE_ESHAPE, "%s: T=%d outside 0..2^20", who, T);
+  REQUIRE(k >= 1 && k <= 64, MOE_EINVAL, "%s: k=%d outside 1..64", who, k);
+  REQUIRE(H >= 1 && H <= kMaxWidth, MOE_ESHAPE, "%s: H=%d outside 1..65536", who, H);
+  REQUIRE(M >= 0 && M <= kMaxPairs, MOE_ESHAPE, "%s: M=%d outside 0..2^20", who, M);
+  return MOE_OK;
+}
+
+bool pairs_ok(int T, int k, int E) {
+  return T >= 0 && k >= 1 && k <= 64 && (long)T * k <= kMaxPairs && E >= 1 && E <= 1024;
+}
+
+moe_status check_q4(const moe_q4* q, const char* who) {
+  REQUIRE(q, MOE_EINVAL, "%s: q4 is NULL", who);
+  REQUIRE(q->K >= 32 && q->K <= kMaxWidth && q->K % 32 == 0 && q->N >= 1 && q->N <= kMaxWidth, MOE_ESHAPE,
+          "%s: K=%d must be a multiple of 32 up to 65536 and N=%d lie in 1..65536", who, q->K, q->N);
+  REQUIRE(q->num >= 1 && q->num <= 1024, MOE_ESHAPE, "%s: num=%d outside 1..1024", who, q->num);
+  REQUIRE(q->group >= 32 && q->group % 32 == 0 && q->K % q->group == 0, MOE_ESHAPE,
+          "%s: group=%d must be a multiple of 32 that divides K=%d", who, q->group, q->K);
+  REQUIRE(q->code == MOE_Q4_INT4 || q->code == MOE_Q4_FP4, MOE_EINVAL, "%s: code=%d", who, q->code);
+  REQUIRE(q->act == MOE_Q4_LINEAR || q->act == MOE_Q4_SWIGLU, MOE_EINVAL, "%s: act=%d", who, q->act);
+  REQUIRE(is_dtype(q->st) || q->st == MOE_SCALE_E8M0, MOE_EINVAL, "%s: bad scale type %d", who, (int)q->st);
+  REQUIRE(q->codes && q->scales, MOE_EINVAL, "%s: codes or scales are NULL", who);
+  REQUIRE(!q->zeros || q->code == MOE_Q4_INT4, MOE_EINVAL, "%s: zero points belong to integer codes", who);
+  const size_t ss = q->st == MOE_SCALE_E8M0 ? 1 : dsize(q->st);
+  REQUIRE(aligned(q->codes, 16) && aligned(q->scales, ss), MOE_EINVAL,
+          "%s: codes must be 16-byte aligned, scales aligned to their element", who);
+  const size_t R = (size_t)q->N * (q->act == MOE_Q4_SWIGLU ? 2 : 1), n = R * (q->K / q->group);
+  REQUIRE(q->num == 1 || (q->code_stride >= R * (q->K / 2) && q->code_stride % 16 == 0), MOE_EINVAL,
+          "%s: code_stride=%zu must be >= %zu and a multiple of 16", who, q->code_stride, R * (q->K / 2));
+  REQUIRE(q->num == 1 || (q->scale_stride >= n * ss && q->scale_stride % ss == 0), MOE_EINVAL,
+          "%s: scale_stride=%zu must be >= %zu and a multiple of the scales' element", who, q->scale_stride, n * ss);
+  REQUIRE(q->num == 1 || !q->zeros || q->zero_stride >= n, MOE_EINVAL, "%s: zero_stride=%zu must be >= %zu", who,
+          q->zero_stride, n);
+  return MOE_OK;
+}
+
+// the buffers of a product of T rows; offsets NULL: one matrix
+moe_status check_q4_call(const moe_q4* q, const void* x, moe_dtype xt, int T, const int32_t* offsets, const void* y,
+                         moe_dtype yt, const char* who) {
+  REQUIRE(x && y, MOE_EINVAL, "%s: NULL pointer", who);
+  REQUIRE(aligned(x, dsize(xt)) && aligned(y, dsize(yt)) && aligned(offsets, 4), MOE_EINVAL,
+          "%s: pointers must be aligned to their element", who);
+  const size_t R = (size_t)q->N * (q->act == MOE_Q4_SWIGLU ? 2 : 1), n = R * (q->K / q->group), last = q->num - 1;
+  const size_t ss = q->st == MOE_SCALE_E8M0 ? 1 : dsize(q->st);
+  const Buffer o{y, (size_t)T * q->N * dsize(yt)};
+  REQUIRE(!overlap(o, {x, (size_t)T * q->K * dsize(xt)}) && !overlap(o, {offsets, (q->num + 1) * (size_t)4}) &&
+              !overlap(o, {q->codes, last * q->code_stride + R * (q->K / 2)}) &&
+              !overlap(o, {q->scales, last * q->scale_stride + n * ss}) &&
+              !overlap(o, {q->zeros, last * q->zero_stride + n}),
+          MOE_EINVAL, "%s: y may overlap no input", who);
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_permute_scratch_bytes(int T, int k, int E) { return pairs_ok(T, k, E) ? permute_scratch_bytes(T, k, E) : 0; }
+
+moe_status moe_permute(const void* x, moe_dtype xt, int T, int k, int H, int E, const int32_t* ids, void* xs,
+                       int32_t* offsets, int32_t* perm, int32_t* rows, void* scratch, size_t scratch_bytes,
+                       moe_stream_t stream) {
+  REQUIRE(k >= 1 && k <= 64, MOE_EINVAL, "moe_permute: k=%d outside 1..64", k);
+  REQUIRE(T >= 0 && (long)T * k <= kMaxPairs, MOE_ESHAPE, "moe_permute: T=%d, k=%d: T*k outside 0..2^20", T, k);
+  REQUIRE(E >= 1 && E <= 1024, MOE_ESHAPE, "moe_permute: E=%d outside 1..1024", E);
+  REQUIRE(!x == !xs, MOE_EINVAL, "moe_permute: x and xs must both be given or both be NULL");
+  REQUIRE(!x || (H >= 1 && H <= kMaxWidth), MOE_ESHAPE, "moe_permute: H=%d outside 1..65536", H);
+  REQUIRE(!x || is_dtype(xt), MOE_EINVAL, "moe_permute: bad dtype %d", (int)xt);
+  REQUIRE(offsets && (T == 0 || (ids && perm && rows)), MOE_EINVAL, "moe_permute: NULL pointer");
+  const size_t P = (size_t)T * k, need = permute_scratch_bytes(T, k, E);
+  REQUIRE((!x || (aligned(x, dsize(xt)) && aligned(xs, dsize(xt)))) && aligned(ids, 4) && aligned(offsets, 4) &&
+              aligned(perm, 4) && aligned(rows, 4) && aligned(scratch, 4),
+          MOE_EINVAL, "moe_permute: pointers must be aligned to their element");
+  REQUIRE(need == 0 || (scratch && scratch_bytes >= need), MOE_ENOMEM, "moe_permute: scratch %zu bytes < %zu needed",
+          scratch ? scratch_bytes : (size_t)0, need);
+  const Buffer in[2] = {{x, x ? (size_t)T * H * dsize(xt) : 0}, {ids, P * 4}};
+  const Buffer outs[5] = {{xs, x ? P * H * dsize(xt) : 0}, {offsets, (E + 1) * (size_t)4}, {perm, P * 4}, {rows, P * 4},
+                          {need ? scratch : nullptr, need}};
+  for (int i = 0; i < 5; ++i) {
+    for (const Buffer& b : in)
+      REQUIRE(!overlap(outs[i], b), MOE_EINVAL, "moe_permute: an output or the scratch overlaps an input");
+    for (int j = 0; j < i; ++j)
+      REQUIRE(!overlap(outs[i], outs[j]), MOE_EINVAL, "moe_permute: outputs and scratch may not overlap each other");
+  }
+  return launch_permute(x, xt, T, k, H, E, ids, xs, offsets, perm, rows, (int32_t*)scratch, (hipStream_t)stream);
+}
+
+moe_status moe_unpermute(const void* ys, moe_dtype yt, int M, const int32_t* rows, const float* w, const void* base,
+                         int T, int k, int H, void* out, moe_dtype ot, moe_stream_t stream) {
+  const moe_status st = check_rows(T, k, H, M, "moe_unpermute");
+  if (st != MOE_OK) return st;
+  REQUIRE(is_dtype(yt) && is_dtype(ot), MOE_EINVAL, "moe_unpermute: bad dtype %d or %d", (int)yt, (int)ot);
+  if (T == 0) return MOE_OK;
+  REQUIRE((ys || M == 0) && rows && out, MOE_EINVAL, "moe_unpermute: NULL pointer");
+  REQUIRE(aligned(ys, dsize(yt)) && aligned(rows, 4) && aligned(w, 4) && aligned(base, dsize(ot)) &&
+              aligned(out, dsize(ot)),
+          MOE_EINVAL, "moe_unpermute: pointers must be aligned to their element");
+  const size_t n = (size_t)T * H, P = (size_t)T * k;
+  const Buffer o{out, n * dsize(ot)};
+  REQUIRE(!overlap_part(o, {base, n * dsize(ot)}) && !overlap(o, {ys, (size_t)M * H * dsize(yt)}) &&
+              !overlap(o, {rows, P * 4}) && !overlap(o, {w, P * 4}),
+          MOE_EINVAL, "moe_unpermute: out may be base, but overlap no input otherwise");
+  return launch_unpermute(ys, yt, M, rows, w, base, T, k, H, out, ot, (hipStream_t)stream);
+}
+
+moe_status moe_unpermute_grad(const void* gout, moe_dtype gt, const void* ys, moe_dtype yt, int M, const int32_t* rows,
+                              const float* w, int T, int k, int H, void* gys, float* gw, moe_stream_t stream) {
+  const moe_status st = check_rows(T, k, H, M, "moe_unpermute_grad");
+  if (st != MOE_OK) return st;
+  REQUIRE(is_dtype(gt) && is_dtype(yt), MOE_EINVAL, "moe_unpermute_grad: bad dtype %d or %d", (int)gt, (int)yt);
+  if (T == 0 || (!gw && (!gys || M == 0))) return MOE_OK;
+  REQUIRE(gout && rows && (!gw || ys || M == 0), MOE_EINVAL, "moe_unpermute_grad: NULL pointer");
+  REQUIRE(aligned(gout, dsize(gt)) && aligned(ys, dsize(yt)) && aligned(rows, 4) && aligned(w, 4) &&
+              aligned(gys, dsize(yt)) && aligned(gw, 4),
+          MOE_EINVAL, "moe_unpermute_grad: pointers must be aligned to their element");
+  const size_t P = (size_t)T * k, m = (size_t)M * H * dsize(yt);
+  const Buffer g{gout, (size_t)T * H * dsize(gt)}, r{rows, P * 4}, wb{w, P * 4}, y{ys, m}, oy{gys, m}, ow{gw, P * 4};
+  REQUIRE(!overlap_part(oy, y) && !overlap(oy, g) && !overlap(oy, r) && !overlap(oy, wb) && !overlap(ow, y) &&
+              !overlap(ow, g) && !overlap(ow, r) && !overlap(ow, wb) && !overlap(oy, ow),
+          MOE_EINVAL, "moe_unpermute_grad: gys may be ys, but no output may overlap an input or the other otherwise");
+  return launch_unpermute_grad(gout, gt, ys, yt, M, rows, w, T, k, H, gys, gw, (hipStream_t)stream);
+}
+
+moe_status moe_route_grad(const moe_router* R, const void* logits, moe_dtype lt, int T, const int32_t* ids,
+                          const float* w, const float* gw, void* glogits, moe_dtype gt, moe_stream_t stream) {
+  const moe_status st = check_router(R, "moe_route_grad");
+  if (st != MOE_OK) return st;
+  REQUIRE(is_dtype(lt) && is_dtype(gt), MOE_EINVAL, "moe_route_grad: bad dtype %d or %d", (int)lt, (int)gt);
+  REQUIRE(T >= 0 && T <= kMaxTokens, MOE_ESHAPE, "moe_route_grad: T=%d outside 0..2^20", T);
+  if (T == 0) return MOE_OK;
+  REQUIRE(logits && ids && w && gw && glogits, MOE_EINVAL, "moe_route_grad: NULL pointer");
+  REQUIRE(aligned(logits, dsize(lt)) && aligned(ids, 4) && aligned(w, 4) && aligned(gw, 4) && aligned(glogits, dsize(gt)),
+          MOE_EINVAL, "moe_route_grad: pointers must be aligned to their element");
+  const size_t n = (size_t)T * R->E, P = (size_t)T * R->k * 4;
+  const Buffer o{glogits, n * dsize(gt)};
+  REQUIRE(!overlap(o, {logits, n * dsize(lt)}) && !overlap(o, {ids, P}) && !overlap(o, {w, P}) && !overlap(o, {gw, P}),
+          MOE_EINVAL, "moe_route_grad: glogits may overlap no input");
+  return launch_route_grad(R, logits, lt, T, ids, w, gw, glogits, gt, (hipStream_t)stream);
+}
+
+moe_status moe_q4_linear(const moe_q4* q, const void* x, moe_dtype xt, int T, void* y, moe_dtype yt,
+                         moe_stream_t stream) {
+  moe_status st = check_q4(q, "moe_q4_linear");
+  if (st != MOE_OK) return st;
+  REQUIRE(is_dtype(xt) && is_dtype(yt), MOE_EINVAL, "moe_q4_linear: bad dtype %d or %d", (int)xt, (int)yt);
+  REQUIRE(T >= 0 && T <= kMaxTokens, MOE_ESHAPE, "moe_q4_linear: T=%d outside 0..2^20", T);
+  if (T == 0) return MOE_OK;
+  if ((st = check_q4_call(q, x, xt, T, nullptr, y, yt, "moe_q4_linear")) != MOE_OK) return st;
+  return launch_q4(q, x, xt, T, nullptr, y, yt, (hipStream_t)stream);
+}
+
+moe_status moe_q4_grouped(const moe_q4* q, const void* x, moe_dtype xt, int P, const int32_t* offsets, void* y,
+                          moe_dtype yt, moe_stream_t stream) {
+  moe_status st = check_q4(q, "moe_q4_grouped");
+  if (st != MOE_OK) return st;
+  REQUIRE(is_dtype(xt) && is_dtype(yt), MOE_EINVAL, "moe_q4_grouped: bad dtype %d or %d", (int)xt, (int)yt);
+  REQUIRE(P >= 0 && P <= kMaxPairs, MOE_ESHAPE, "moe_q4_grouped: P=%d outside 0..2^20", P);
+  if (P == 0) return MOE_OK;
+  REQUIRE(offsets, MOE_EINVAL, "moe_q4_grouped: NULL pointer");
+  if ((st = check_q4_call(q, x, xt, P, offsets, y, yt, "moe_q4_grouped")) != MOE_OK) return st;
+  return launch_q4(q, x, xt, P, offsets, y, yt, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,254 @@
+// Products with matrices of 4-bit codes and a scale per group of inputs
+// (moe_q4_linear, moe_q4_grouped), on bf16 MFMA.
+//
+// Codes become bf16 exactly (integers up to 15 off a zero point, E2M1 values); bf16 x
+// is taken as it is and fp32 x as three bf16 parts that hold all its bits, so every
+// product is exact.  A group's products are summed by the matrix units in fp32, then
+// scaled and added to the row's sum.
+#include "chunk_dev.h"
+
+namespace moe {
+
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+struct Q4Args {
+  const void* x;
+  const uint8_t *codes, *zeros;
+  const void* scales;
+  void* y;
+  const int32_t* offsets;  // NULL: one matrix
+  int T, K, N, num, group, groups, st;
+  bool swiglu, ybf;
+  size_t code_stride, scale_stride, zero_stride;
+};
+
+__device__ __forceinline__ v8bf as_bf(u32x4_t v) { return __builtin_bit_cast(v8bf, v); }
+
+// A lane's eight codes of one dword as bf16, in order.
+template <bool FP4>
+__device__ __forceinline__ v8bf codes_to_bf16(uint32_t d, float zero) {
+  if constexpr (FP4) {
+    return as_bf(u32x4_t{fp4x2_to_bf16x2<0>(d), fp4x2_to_bf16x2<1>(d), fp4x2_to_bf16x2<2>(d), fp4x2_to_bf16x2<3>(d)});
+  } else {
+    u32x4_t r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r[i] = pack2((float)((d >> (8 * i)) & 15u) - zero, (float)((d >> (8 * i + 4)) & 15u) - zero);
+    return as_bf(r);
+  }
+}
+
+// Eight consecutive elements of x as one or three bf16 parts.  fp32 by truncation:
+// each part takes eight bits and what is left over is exact.
+template <bool XF32>
+struct XPart {
+  static constexpr int kParts = XF32 ? 3 : 1;
+  v8bf p[kParts];
+  __device__ __forceinline__ void load(const void* x, size_t at) {
+    if constexpr (!XF32) {
+      const uint4 h = ld8h((const uint16_t*)x + at);
+      p[0] = as_bf(u32x4_t{h.x, h.y, h.z, h.w});
+    } else {
+      f32x8 f = ld8f((const float*)x + at);
+#pragma unroll
+      for (int part = 0; part < 3; ++part) {
+        u32x4_t r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t lo = __float_as_uint(f[2 * i]), hi = __float_as_uint(f[2 * i + 1]);
+          r[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
+          f[2 * i] -= __uint_as_float(lo & 0xffff0000u);
+          f[2 * i + 1] -= __uint_as_float(hi & 0xffff0000u);
+        }
+        p[part] = as_bf(r);
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ float load_scale(const void* p, int st, size_t at) {
+  if (st == MOE_F32) return ((const float*)p)[at];
+  if (st == MOE_BF16) return bf(((const uint16_t*)p)[at]);
+  return e8m0_to_f32(((const uint8_t*)p)[at]);
+}
+
+// Four lanes that hold a row's chunks (lane 16 q + c: chunk q, dword j in d[j]) exchange
+// them so that d[j] is dword q of chunk j.
+__device__ __forceinline__ void transpose4(uint32_t (&d)[4]) {
+  auto swap16 = [](uint32_t& a, uint32_t& b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0], b = r[1];
+  };
+  auto swap32 = [](uint32_t& a, uint32_t& b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0], b = r[1];
+  };
+  swap16(d[0], d[1]);
+  swap16(d[2], d[3]);
+  swap32(d[0], d[2]);
+  swap32(d[1], d[3]);
+}
+
+// The matrix and the rows of the row tile that a workgroup takes: tile `tile` of 16 TT
+// rows, counted over the matrices.  False: there is none.
+struct Tile {
+  int e, row, rows;
+};
+
+__device__ __forceinline__ bool find_tile(const Q4Args& a, int tile, int size, Tile& o) {
+  if (!a.offsets) {
+    o = {0, tile * size, min(size, a.T - tile * size)};
+    return o.rows > 0;
+  }
+  const int lane = threadIdx.x & 63;
+  int before = 0;  // tiles of the matrices so far
+  for (int e0 = 0; e0 < a.num; e0 += 64) {
+    const int e = e0 + lane;
+    const int lo = min(max(e < a.num ? a.offsets[e] : 0, 0), a.T);
+    const int hi = min(max(e < a.num ? a.offsets[e + 1] : 0, lo), a.T);
+    const int mine = (hi - lo + size - 1) / size;
+    int incl = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int v = __shfl_up(incl, off, 64);
+      if (lane >= off) incl += v;
+    }
+    const int start = before + incl - mine;
+    const uint64_t hit = __ballot(tile >= start && tile < start + mine);
+    if (hit) {
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      const int row = __builtin_amdgcn_readlane(lo, l) + (tile - __builtin_amdgcn_readlane(start, l)) * size;
+      o = {e0 + l, row, min(size, __builtin_amdgcn_readlane(hi, l) - row)};
+      return true;
+    }
+    before = __builtin_amdgcn_readfirstlane(__shfl(before + incl, 63, 64));
+  }
+  return false;
+}
+
+constexpr int kWaves = 8;
+constexpr int kTilesY = 32768;  // row tiles along a grid's second dimension
+
+// 16 outputs (SWIGLU: and the 16 above them) for up to 16 TT rows of x.  The wavefronts
+// take blocks of 128 inputs in turn; their sums meet in LDS.  MFMA 16x16x32: lane l
+// supplies row (x) or column (codes) l % 16 at inputs 8 (l / 16) on, and gets rows
+// 4 (l / 16) + i of column l % 16.
+template <bool XF32, bool FP4, int TT, bool GLU>
+__global__ __launch_bounds__(64 * kWaves) void q4_rows_kernel(Q4Args a) {
+  constexpr int NT = GLU ? 2 : 1;
+  __shared__ float red[kWaves][NT * TT * 256];
+  Tile tile;
+  if (!find_tile(a, blockIdx.z * kTilesY + blockIdx.y, 16 * TT, tile)) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
+  const int n = min((int)blockIdx.x * 16 + c, a.N - 1);
+  const uint8_t* codes = a.codes + tile.e * a.code_stride;
+  const uint8_t* scales = (const uint8_t*)a.scales + tile.e * a.scale_stride;
+  const uint8_t* zeros = a.zeros ? a.zeros + tile.e * a.zero_stride : nullptr;
+  size_t xrow[TT];
+#pragma unroll
+  for (int i = 0; i < TT; ++i) xrow[i] = (size_t)(tile.row + min(16 * i + c, tile.rows - 1)) * a.K;
+  v4f acc[NT][TT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[i][t] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int k0 = wave * 128; k0 < a.K; k0 += kWaves * 128) {
+    uint32_t d[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const uint4 v = ld_stream16(codes + (size_t)(n + i * a.N) * (a.K / 2) + min(k0 / 2 + 16 * q, a.K / 2 - 16));
+      d[i][0] = v.x, d[i][1] = v.y, d[i][2] = v.z, d[i][3] = v.w;
+      transpose4(d[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + 32 * j;
+      if (k >= a.K) break;
+      const int g = k / a.group;
+      v8bf w[NT];
+      float s[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const size_t at = (size_t)(n + i * a.N) * a.groups + g;
+        s[i] = load_scale(scales, a.st, at);
+        w[i] = codes_to_bf16<FP4>(d[i][j], FP4 ? 0.f : zeros ? (float)zeros[at] : 8.f);
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        XPart<XF32> x;
+        x.load(a.x, xrow[t] + k + 8 * q);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          v4f part = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int p = XPart<XF32>::kParts - 1; p >= 0; --p)
+            part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.p[p], w[i], part, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][t][r] = fmaf(s[i], part[r], acc[i][t][r]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) *(v4f*)&red[wave][((i * TT + t) * 64 + lane) * 4] = acc[i][t];
+  __syncthreads();
+  for (int o = threadIdx.x; o < TT * 256; o += 64 * kWaves) {
+    const int t = o >> 8, r = (o >> 4) & 15, col = o & 15;  // row r and column col of row tile t
+    const int at = (t * 64 + (r >> 2) * 16 + col) * 4 + (r & 3);
+    float v[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      v[i] = 0.f;
+#pragma unroll
+      for (int u = 0; u < kWaves; ++u) v[i] += red[u][i * TT * 256 + at];
+    }
+    if (GLU) v[0] *= gate_sigmoid(v[0]) * v[NT - 1];
+    const int out = blockIdx.x * 16 + col, row = 16 * t + r;
+    if (out < a.N && row < tile.rows) {
+      const size_t to = (size_t)(tile.row + row) * a.N + out;
+      if (a.ybf)
+        ((uint16_t*)a.y)[to] = bf16_of(v[0]);
+      else
+        ((float*)a.y)[to] = v[0];
+    }
+  }
+}
+
+template <bool XF32, bool FP4, int TT>
+void run_rows(const Q4Args& a, hipStream_t s) {
+  const int size = 16 * TT;
+  // a matrix's last tile may be short: at most one such a matrix that has rows
+  const int tiles = a.offsets ? a.T / size + min(a.num, a.T) : (a.T + size - 1) / size;
+  const dim3 grid((a.N + 15) / 16, min(tiles, kTilesY), (tiles + kTilesY - 1) / kTilesY), block(64 * kWaves);
+  if (a.swiglu)
+    launch(MOE_PROF_Q4, q4_rows_kernel<XF32, FP4, TT, true>, grid, block, 0, s, a);
+  else
+    launch(MOE_PROF_Q4, q4_rows_kernel<XF32, FP4, TT, false>, grid, block, 0, s, a);
+}
+
+template <bool XF32, bool FP4>
+void run_q4(const Q4Args& a, hipStream_t s) {
+  run_rows<XF32, FP4, 1>(a, s);
+}
+
+}  // namespace
+
+moe_status launch_q4(const moe_q4* q, const void* x, moe_dtype xt, int T, const int32_t* offsets, void* y, moe_dtype yt,
+                     hipStream_t s) {
+  const Q4Args a{x, q->codes, q->zeros, q->scales, y, offsets, T, q->K, q->N, q->num, q->group, q->K / q->group, q->st,
+                 q->act == MOE_Q4_SWIGLU, yt == MOE_BF16, q->code_stride, q->scale_stride, q->zero_stride};
+  const bool xf = xt == MOE_F32, fp4 = q->code == MOE_Q4_FP4;
+  if (xf)
+    fp4 ? run_q4<true, true>(a, s) : run_q4<true, false>(a, s);
+  else
+    fp4 ? run_q4<false, true>(a, s) : run_q4<false, false>(a, s);
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+}  // namespace moe

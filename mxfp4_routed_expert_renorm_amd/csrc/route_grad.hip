@@ -1,0 +1,141 @@
+// The gradient of a router's weights with respect to its logits, the picks being
+// fixed (moe_route_grad).  With g the gradient of the weights w and m = sum g w / sum w
+// over the picks (renormalised weights; else 0):
+//   sigmoid  w (1 - s) (g - m) at the picks,   softmax, renormalised  w (g - m) at the picks,
+//   softmax  sum over e's picks of g w - s[e] sum g w  at every expert e.
+// Dividing by sum w, not by the scale, makes m the weights' own mean: a part common to
+// all g cancels to the last bit however w was rounded.
+//
+// One wavefront per token: lane i holds pick i, and expert 4 (lane + 64 j) + i is
+// element i of a lane's vector j, so that a row leaves in 16-byte stores.
+#include "chunk_dev.h"
+
+namespace moe {
+
+namespace {
+
+constexpr float kLowestLogit = -0x1.fep127f;  // bf16's lowest value: a logit there or below masks its expert
+
+struct RouteGradArgs {
+  const void* logits;
+  const int32_t* ids;
+  const float *w, *gw;
+  void* out;
+  int T, E, k;
+  bool lbf, obf, sigmoid, renorm;
+};
+
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+// V: vectors of four experts a lane.  DENSE: every expert has a gradient.
+template <int V, bool DENSE>
+__global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int t = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  if (t >= a.T) return;
+  const size_t row = (size_t)t * a.E;
+  f32x4 d[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * (lane + 64 * j) + i;
+      d[j][i] = DENSE ? (e < a.E ? load1(a.logits, a.lbf, row + e) : -INFINITY) : 0.f;
+    }
+  }
+  // the picks, one a lane
+  int id = -1;
+  float w = 0.f, g = 0.f, rest = 1.f;
+  if (lane < a.k) {
+    id = a.ids[(size_t)t * a.k + lane];
+    w = a.w[(size_t)t * a.k + lane];
+    g = a.gw[(size_t)t * a.k + lane];
+  }
+  const bool live = (uint32_t)id < (uint32_t)a.E && w != 0.f;
+  if (!live) w = g = 0.f;
+  if (a.sigmoid && live) rest = gate_sigmoid(-load1(a.logits, a.lbf, row + id));
+  const double all = wave_sum_f64((double)g * w);
+  if constexpr (DENSE) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, d[j][i]);  // a NaN is no maximum
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = d[j][i];
+        d[j][i] = x > kLowestLogit ? (x == top ? 1.f : expf(x - top)) : 0.f;  // not for NaN either
+        sum += d[j][i];
+      }
+    sum = wave_sum(sum);
+    const float f = sum > 0.f ? -(float)(all / (double)sum) : 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] *= f;
+  }
+  double mean = 0.0;
+  if (a.renorm) {
+    const double total = wave_sum_f64((double)w);
+    mean = total != 0.0 ? all / total : 0.0;
+  }
+  const float mine = w * rest * (float)(g - mean);
+  for (int i = 0; i < a.k; ++i) {
+    const int e = __builtin_amdgcn_readlane(id, i);
+    const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(live ? mine : 0.f), i));
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (e == 4 * (lane + 64 * j) + n) d[j][n] += v;
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int e = 4 * (lane + 64 * j);
+    if (a.obf) {
+      uint16_t* o = (uint16_t*)a.out + row + e;
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (e + n < a.E) o[n] = bf16_of(d[j][n]);
+    } else {
+      float* o = (float*)a.out + row + e;
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (e + n < a.E) o[n] = d[j][n];
+    }
+  }
+}
+
+template <int V>
+void run(const RouteGradArgs& a, hipStream_t s) {
+  const dim3 grid((a.T + 3) / 4), block(256);
+  if (a.sigmoid || a.renorm)
+    launch(MOE_PROF_ROUTE, route_grad_kernel<V, false>, grid, block, 0, s, a);
+  else
+    launch(MOE_PROF_ROUTE, route_grad_kernel<V, true>, grid, block, 0, s, a);
+}
+
+}  // namespace
+
+moe_status launch_route_grad(const moe_router* R, const void* logits, moe_dtype lt, int T, const int32_t* ids,
+                             const float* w, const float* gw, void* glogits, moe_dtype gt, hipStream_t s) {
+  const RouteGradArgs a{logits, ids, w,  gw, glogits, T, R->E, R->k, lt == MOE_BF16, gt == MOE_BF16,
+                        R->scoring == MOE_SCORE_SIGMOID, R->renorm != 0};
+  if (R->E <= 256)
+    run<1>(a, s);
+  else if (R->E <= 512)
+    run<2>(a, s);
+  else
+    run<4>(a, s);
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+}  // namespace moe
