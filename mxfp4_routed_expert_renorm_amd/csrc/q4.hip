@@ -5,132 +5,15 @@
 // is taken as it is and fp32 x as three bf16 parts that hold all its bits, so every
 // product is exact.  A group's products are summed by the matrix units in fp32, then
 // scaled and added to the row's sum.
-#include "chunk_dev.h"
+#include "q4_dev.h"
 
 namespace moe {
 
 namespace {
 
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-
-struct Q4Args {
-  const void* x;
-  const uint8_t *codes, *zeros;
-  const void* scales;
-  void* y;
-  const int32_t* offsets;  // NULL: one matrix
-  int T, K, N, num, group, groups, st;
-  bool swiglu, ybf;
-  size_t code_stride, scale_stride, zero_stride;
-};
-
-__device__ __forceinline__ v8bf as_bf(u32x4_t v) { return __builtin_bit_cast(v8bf, v); }
-
-// A lane's eight codes of one dword as bf16, in order.
-template <bool FP4>
-__device__ __forceinline__ v8bf codes_to_bf16(uint32_t d, float zero) {
-  if constexpr (FP4) {
-    return as_bf(u32x4_t{fp4x2_to_bf16x2<0>(d), fp4x2_to_bf16x2<1>(d), fp4x2_to_bf16x2<2>(d), fp4x2_to_bf16x2<3>(d)});
-  } else {
-    u32x4_t r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r[i] = pack2((float)((d >> (8 * i)) & 15u) - zero, (float)((d >> (8 * i + 4)) & 15u) - zero);
-    return as_bf(r);
-  }
-}
-
-// Eight consecutive elements of x as one or three bf16 parts.  fp32 by truncation:
-// each part takes eight bits and what is left over is exact.
-template <bool XF32>
-struct XPart {
-  static constexpr int kParts = XF32 ? 3 : 1;
-  v8bf p[kParts];
-  __device__ __forceinline__ void load(const void* x, size_t at) {
-    if constexpr (!XF32) {
-      const uint4 h = ld8h((const uint16_t*)x + at);
-      p[0] = as_bf(u32x4_t{h.x, h.y, h.z, h.w});
-    } else {
-      f32x8 f = ld8f((const float*)x + at);
-#pragma unroll
-      for (int part = 0; part < 3; ++part) {
-        u32x4_t r;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t lo = __float_as_uint(f[2 * i]), hi = __float_as_uint(f[2 * i + 1]);
-          r[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
-          f[2 * i] -= __uint_as_float(lo & 0xffff0000u);
-          f[2 * i + 1] -= __uint_as_float(hi & 0xffff0000u);
-        }
-        p[part] = as_bf(r);
-      }
-    }
-  }
-};
-
-__device__ __forceinline__ float load_scale(const void* p, int st, size_t at) {
-  if (st == MOE_F32) return ((const float*)p)[at];
-  if (st == MOE_BF16) return bf(((const uint16_t*)p)[at]);
-  return e8m0_to_f32(((const uint8_t*)p)[at]);
-}
-
-// Four lanes that hold a row's chunks (lane 16 q + c: chunk q, dword j in d[j]) exchange
-// them so that d[j] is dword q of chunk j.
-__device__ __forceinline__ void transpose4(uint32_t (&d)[4]) {
-  auto swap16 = [](uint32_t& a, uint32_t& b) {
-    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-    a = r[0], b = r[1];
-  };
-  auto swap32 = [](uint32_t& a, uint32_t& b) {
-    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    a = r[0], b = r[1];
-  };
-  swap16(d[0], d[1]);
-  swap16(d[2], d[3]);
-  swap32(d[0], d[2]);
-  swap32(d[1], d[3]);
-}
-
-// The matrix and the rows of the row tile that a workgroup takes: tile `tile` of 16 TT
-// rows, counted over the matrices.  False: there is none.
-struct Tile {
-  int e, row, rows;
-};
-
-__device__ __forceinline__ bool find_tile(const Q4Args& a, int tile, int size, Tile& o) {
-  if (!a.offsets) {
-    o = {0, tile * size, min(size, a.T - tile * size)};
-    return o.rows > 0;
-  }
-  const int lane = threadIdx.x & 63;
-  int before = 0;  // tiles of the matrices so far
-  for (int e0 = 0; e0 < a.num; e0 += 64) {
-    const int e = e0 + lane;
-    const int lo = min(max(e < a.num ? a.offsets[e] : 0, 0), a.T);
-    const int hi = min(max(e < a.num ? a.offsets[e + 1] : 0, lo), a.T);
-    const int mine = (hi - lo + size - 1) / size;
-    int incl = mine;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int v = __shfl_up(incl, off, 64);
-      if (lane >= off) incl += v;
-    }
-    const int start = before + incl - mine;
-    const uint64_t hit = __ballot(tile >= start && tile < start + mine);
-    if (hit) {
-      const int l = __ffsll((unsigned long long)hit) - 1;
-      const int row = __builtin_amdgcn_readlane(lo, l) + (tile - __builtin_amdgcn_readlane(start, l)) * size;
-      o = {e0 + l, row, min(size, __builtin_amdgcn_readlane(hi, l) - row)};
-      return true;
-    }
-    before = __builtin_amdgcn_readfirstlane(__shfl(before + incl, 63, 64));
-  }
-  return false;
-}
+using namespace q4;
 
 constexpr int kWaves = 8;
-constexpr int kTilesY = 32768;  // row tiles along a grid's second dimension
 
 // 16 outputs (SWIGLU: and the 16 above them) for up to 16 TT rows of x.  The wavefronts
 // take blocks of 128 inputs in turn; their sums meet in LDS.  MFMA 16x16x32: lane l
@@ -233,6 +116,10 @@ void run_rows(const Q4Args& a, hipStream_t s) {
 
 template <bool XF32, bool FP4>
 void run_q4(const Q4Args& a, hipStream_t s) {
+  if (a.T > 64) {
+    launch_q4_tile(a, XF32, FP4, s);
+    return;
+  }
   run_rows<XF32, FP4, 1>(a, s);
 }
 
