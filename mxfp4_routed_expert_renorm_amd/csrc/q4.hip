@@ -24,7 +24,7 @@ __global__ __launch_bounds__(64 * kWaves) void q4_rows_kernel(Q4Args a) {
   constexpr int NT = GLU ? 2 : 1;
   __shared__ float red[kWaves][NT * TT * 256];
   Tile tile;
-  if (!find_tile(a, blockIdx.z * kTilesY + blockIdx.y, 16 * TT, tile)) return;
+  if (!find_tile<false>(a, blockIdx.z * kTilesY + blockIdx.y, 16 * TT, tile)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
   const int n = min((int)blockIdx.x * 16 + c, a.N - 1);
   const uint8_t* codes = a.codes + tile.e * a.code_stride;
@@ -50,13 +50,13 @@ __global__ __launch_bounds__(64 * kWaves) void q4_rows_kernel(Q4Args a) {
     for (int j = 0; j < 4; ++j) {
       const int k = k0 + 32 * j;
       if (k >= a.K) break;
-      const int g = k / a.group;
+      const int g = group_of(a, k / 32);
       v8bf w[NT];
       float s[NT];
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const size_t at = (size_t)(n + i * a.N) * a.groups + g;
-        s[i] = load_scale(scales, a.st, at);
+        s[i] = scale_of(raw_scale(scales, a.st, at), a.st);
         w[i] = codes_to_bf16<FP4>(d[i][j], FP4 ? 0.f : zeros ? (float)zeros[at] : 8.f);
       }
 #pragma unroll
@@ -116,7 +116,7 @@ void run_rows(const Q4Args& a, hipStream_t s) {
 
 template <bool XF32, bool FP4>
 void run_q4(const Q4Args& a, hipStream_t s) {
-  if (a.T > 64) {
+  if (a.T > 64 && (uintptr_t)a.x % 16 == 0) {
     launch_q4_tile(a, XF32, FP4, s);
     return;
   }
@@ -128,7 +128,8 @@ void run_q4(const Q4Args& a, hipStream_t s) {
 moe_status launch_q4(const moe_q4* q, const void* x, moe_dtype xt, int T, const int32_t* offsets, void* y, moe_dtype yt,
                      hipStream_t s) {
   const Q4Args a{x, q->codes, q->zeros, q->scales, y, offsets, T, q->K, q->N, q->num, q->group, q->K / q->group, q->st,
-                 q->act == MOE_Q4_SWIGLU, yt == MOE_BF16, q->code_stride, q->scale_stride, q->zero_stride};
+                 q->act == MOE_Q4_SWIGLU, yt == MOE_BF16, q->code_stride, q->scale_stride, q->zero_stride,
+                 q->group == 32 ? 0u : (uint32_t)(((uint64_t)1 << 32) / (q->group / 32)) + 1, q->group == 32};
   const bool xf = xt == MOE_F32, fp4 = q->code == MOE_Q4_FP4;
   if (xf)
     fp4 ? run_q4<true, true>(a, s) : run_q4<true, false>(a, s);

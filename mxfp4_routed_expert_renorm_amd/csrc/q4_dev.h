@@ -22,6 +22,8 @@ struct Q4Args {
   int T, K, N, num, group, groups, st;
   bool swiglu, ybf;
   size_t code_stride, scale_stride, zero_stride;
+  uint32_t magic;  // 2^32 / (group / 32), rounded up, less 2^32 where that is its size
+  int unit;        // 1: groups of 32, else 0
 };
 
 __device__ __forceinline__ v8bf as_bf(u32x4_t v) { return __builtin_bit_cast(v8bf, v); }
@@ -82,11 +84,20 @@ struct XPart {
   }
 };
 
-__device__ __forceinline__ float load_scale(const void* p, int st, size_t at) {
-  if (st == MOE_F32) return ((const float*)p)[at];
-  if (st == MOE_BF16) return bf(((const uint16_t*)p)[at]);
-  return e8m0_to_f32(((const uint8_t*)p)[at]);
+// A scale as it is stored, and its value: nothing between the loads of a batch waits for
+// one of them.
+__device__ __forceinline__ uint32_t raw_scale(const void* p, int st, size_t at) {
+  if (st == MOE_F32) return ((const uint32_t*)p)[at];
+  if (st == MOE_BF16) return ((const uint16_t*)p)[at];
+  return ((const uint8_t*)p)[at];
 }
+
+__device__ __forceinline__ float scale_of(uint32_t raw, int st) {
+  return st == MOE_F32 ? __uint_as_float(raw) : st == MOE_BF16 ? __uint_as_float(raw << 16) : e8m0_to_f32(raw);
+}
+
+// The group of the inputs from 32 c on.
+__device__ __forceinline__ int group_of(const Q4Args& a, int c) { return (int)__umulhi((uint32_t)c, a.magic) + c * a.unit; }
 
 // Four lanes that hold a row's chunks (lane 16 q + c: chunk q, dword j in d[j]) exchange
 // them so that d[j] is dword q of chunk j.
@@ -105,39 +116,47 @@ __device__ __forceinline__ void transpose4(uint32_t (&d)[4]) {
   swap32(d[1], d[3]);
 }
 
-// The matrix and the rows of the row tile that a workgroup takes: tile `tile` of 16 TT
-// rows, counted over the matrices.  False: there is none.
+// The matrix and the rows of the row tile that a workgroup takes, of `size` rows each but
+// for a matrix's last.  False: there is none.
 struct Tile {
   int e, row, rows;
 };
 
+// LARGE: tiles of more than half the size come first, so that the chip does not end on
+// them alone.
+template <bool LARGE>
 __device__ __forceinline__ bool find_tile(const Q4Args& a, int tile, int size, Tile& o) {
   if (!a.offsets) {
     o = {0, tile * size, min(size, a.T - tile * size)};
     return o.rows > 0;
   }
   const int lane = threadIdx.x & 63;
-  int before = 0;  // tiles of the matrices so far
-  for (int e0 = 0; e0 < a.num; e0 += 64) {
-    const int e = e0 + lane;
-    const int lo = min(max(e < a.num ? a.offsets[e] : 0, 0), a.T);
-    const int hi = min(max(e < a.num ? a.offsets[e + 1] : 0, lo), a.T);
-    const int mine = (hi - lo + size - 1) / size;
-    int incl = mine;
+  int before = 0;  // tiles so far
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int v = __shfl_up(incl, off, 64);
-      if (lane >= off) incl += v;
+  for (int pass = 0; pass < (LARGE ? 2 : 1); ++pass) {
+    for (int e0 = 0; e0 < a.num; e0 += 64) {
+      const int e = e0 + lane;
+      const int lo = min(max(e < a.num ? a.offsets[e] : 0, 0), a.T);
+      const int hi = min(max(e < a.num ? a.offsets[e + 1] : 0, lo), a.T);
+      const int all = (hi - lo + size - 1) / size, first = LARGE ? (hi - lo + size / 2 - 1) / size : all;
+      const int mine = pass ? all - first : first;
+      int incl = mine;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int v = __shfl_up(incl, off, 64);
+        if (lane >= off) incl += v;
+      }
+      const int start = before + incl - mine;
+      const uint64_t hit = __ballot(tile >= start && tile < start + mine);
+      if (hit) {
+        const int l = __ffsll((unsigned long long)hit) - 1;
+        const int in = tile - __builtin_amdgcn_readlane(start, l) + (pass ? __builtin_amdgcn_readlane(first, l) : 0);
+        const int row = __builtin_amdgcn_readlane(lo, l) + in * size;
+        o = {e0 + l, row, min(size, __builtin_amdgcn_readlane(hi, l) - row)};
+        return true;
+      }
+      before = __builtin_amdgcn_readfirstlane(__shfl(before + incl, 63, 64));
     }
-    const int start = before + incl - mine;
-    const uint64_t hit = __ballot(tile >= start && tile < start + mine);
-    if (hit) {
-      const int l = __ffsll((unsigned long long)hit) - 1;
-      const int row = __builtin_amdgcn_readlane(lo, l) + (tile - __builtin_amdgcn_readlane(start, l)) * size;
-      o = {e0 + l, row, min(size, __builtin_amdgcn_readlane(hi, l) - row)};
-      return true;
-    }
-    before = __builtin_amdgcn_readfirstlane(__shfl(before + incl, 63, 64));
   }
   return false;
 }
