@@ -2,6 +2,8 @@
 // codes' and inputs' ways to bf16, and the search for a row tile's matrix.
 #pragma once
 
+#include <type_traits>
+
 #include "chunk_dev.h"
 
 namespace moe {
@@ -44,6 +46,17 @@ __device__ __forceinline__ v8bf codes_to_bf16(uint32_t d, float zero) {
     return as_bf(u32x4_t{pack2(e0[0] - zero, o0[0] - zero), pack2(e0[1] - zero, o0[1] - zero),
                          pack2(e1[0] - zero, o1[0] - zero), pack2(e1[1] - zero, o1[1] - zero)});
   }
+}
+
+// Integer codes 0..15 as they are: the same convert straight to bf16
+__device__ __forceinline__ v8bf int4_to_bf16(uint32_t d) {
+  const uint32_t even = d & 0x0f0f0f0fu, odd = (d >> 4) & 0x0f0f0f0fu;
+  const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400), hi = __builtin_amdgcn_perm(odd, even, 0x07030602);
+  auto two = [](uint32_t v, auto word) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.f, decltype(word)::value));
+  };
+  return as_bf(u32x4_t{two(lo, std::false_type{}), two(lo, std::true_type{}), two(hi, std::false_type{}),
+                       two(hi, std::true_type{})});
 }
 
 // E2M1 codes with their block's power of two: exact
@@ -116,6 +129,17 @@ __device__ __forceinline__ void transpose4(uint32_t (&d)[4]) {
   swap32(d[1], d[3]);
 }
 
+// sum of the lanes up to this one
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, dpp::kRowBcast15, 0xa, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, dpp::kRowBcast31, 0xc, 0xf, false);
+  return v;
+}
+
 // The matrix and the rows of the row tile that a workgroup takes, of `size` rows each but
 // for a matrix's last.  False: there is none.
 struct Tile {
@@ -135,18 +159,10 @@ __device__ __forceinline__ bool find_tile(const Q4Args& a, int tile, int size, T
 #pragma unroll
   for (int pass = 0; pass < (LARGE ? 2 : 1); ++pass) {
     for (int e0 = 0; e0 < a.num; e0 += 64) {
-      const int e = e0 + lane;
-      const int lo = min(max(e < a.num ? a.offsets[e] : 0, 0), a.T);
-      const int hi = min(max(e < a.num ? a.offsets[e + 1] : 0, lo), a.T);
+      const int e = e0 + lane, from = a.offsets[min(e, a.num)], to = a.offsets[min(e + 1, a.num)];
+      const int lo = min(max(from, 0), a.T), hi = min(max(to, lo), a.T);  // past the last: no rows
       const int all = (hi - lo + size - 1) / size, first = LARGE ? (hi - lo + size / 2 - 1) / size : all;
-      const int mine = pass ? all - first : first;
-      int incl = mine;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int v = __shfl_up(incl, off, 64);
-        if (lane >= off) incl += v;
-      }
-      const int start = before + incl - mine;
+      const int mine = pass ? all - first : first, incl = wave_scan(mine), start = before + incl - mine;
       const uint64_t hit = __ballot(tile >= start && tile < start + mine);
       if (hit) {
         const int l = __ffsll((unsigned long long)hit) - 1;
@@ -155,7 +171,7 @@ __device__ __forceinline__ bool find_tile(const Q4Args& a, int tile, int size, T
         o = {e0 + l, row, min(size, __builtin_amdgcn_readlane(hi, l) - row)};
         return true;
       }
-      before = __builtin_amdgcn_readfirstlane(__shfl(before + incl, 63, 64));
+      before = __builtin_amdgcn_readlane(before + incl, 63);
     }
   }
   return false;

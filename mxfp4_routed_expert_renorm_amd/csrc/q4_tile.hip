@@ -7,8 +7,6 @@
 // registers: the compiler cannot count such loads among direct ones and waits for all.
 // Codes are converted where they are used: twice for the two halves of the rows, which
 // costs less than bf16 through LDS.
-#include <type_traits>
-
 #include "q4_dev.h"
 
 namespace moe {
