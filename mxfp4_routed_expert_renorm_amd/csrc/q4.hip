@@ -5,7 +5,6 @@
 // is taken as it is and fp32 x as three bf16 parts that hold all its bits, so every
 // product is exact.  A group's products are summed by the matrix units in fp32, then
 // scaled and added to the row's sum.
-#include <cstdlib>
 #include "q4_dev.h"
 
 namespace moe {
@@ -31,10 +30,9 @@ enum {
 // two, and at 16 bytes of codes a lane that bounds the kernel before the memory does.  So
 // codes and x come row by row and go through LDS to the lanes that take them, and the lanes
 // of a row load the scales of different blocks and exchange them.
-template <bool XF32, bool FP4, int MODE>
+template <bool XF32, bool FP4, int MODE, int W>
 struct Rows {
-  static constexpr int W = 8;                             // wavefronts
-  static constexpr int U = !FP4 && MODE == kChunk ? 2 : 4;  // blocks a turn, as many as registers allow
+  static constexpr int U = (!FP4 && MODE == kChunk) || W == 16 ? 2 : 4;  // blocks a turn, as many as registers allow
   static constexpr int kPieces = 4 * U;                   // of 16 bytes of codes a row and turn
   // Zero points: sum q x - z sum x with the sum of x from a matrix of ones, which costs the
   // matrix units one instruction, or, where that would be three, off the codes, which costs
@@ -295,12 +293,12 @@ struct Rows {
   }
 };
 
-template <bool XF32, bool FP4, int MODE>
-__global__ __launch_bounds__(512, 4) void q4_rows_kernel(Q4Args a) {
+template <bool XF32, bool FP4, int MODE, int W>
+__global__ __launch_bounds__(64 * W, 4) void q4_rows_kernel(Q4Args a) {
   // all arguments at once, not one after the other as they are needed
   asm volatile("" ::"s"(a.x), "s"(a.codes), "s"(a.scales), "s"(a.zeros), "s"(a.y), "s"(a.offsets), "s"(a.T), "s"(a.K),
                "s"(a.N), "s"(a.st), "s"(a.groups), "s"(a.magic), "s"(a.unit));
-  typedef Rows<XF32, FP4, MODE> Kernel;
+  typedef Rows<XF32, FP4, MODE, W> Kernel;
   __shared__ typename Kernel::Smem sm;
   Tile tile;
   if (!find_tile<false>(a, blockIdx.z * kTilesY + blockIdx.y, 16, tile)) return;
@@ -309,17 +307,38 @@ __global__ __launch_bounds__(512, 4) void q4_rows_kernel(Q4Args a) {
 
 template <bool XF32, bool FP4, int MODE>
 void run_rows(const Q4Args& a, hipStream_t s) {
-  // a matrix's last tile may be short: at most one such a matrix that has rows
-  const int tiles = a.offsets ? a.T / 16 + min(a.num, a.T) : (a.T + 15) / 16;
-  const dim3 grid((a.N + 15) / 16, min(tiles, kTilesY), (tiles + kTilesY - 1) / kTilesY);
-  launch(MOE_PROF_Q4, q4_rows_kernel<XF32, FP4, MODE>, grid, dim3(512), 0, s, a);
+  const int tiles = tile_groups(a, 16), cols = (a.N + 15) / 16;
+  const dim3 grid(cols, min(tiles, kTilesY), (tiles + kTilesY - 1) / kTilesY);
+  // Twice the wavefronts where a compute unit has one workgroup only: a wavefront's blocks are
+  // a chain of waits.  One token, 4096 inputs, 2048 outputs 5.1 us against 5.4, 4096 5.8
+  // against 6.1; 8192 9.9 against 8.6, 64 rows of 64 experts 86 against 63.
+  if ((long)cols * tiles <= 256)
+    launch(MOE_PROF_Q4, q4_rows_kernel<XF32, FP4, MODE, 16>, grid, dim3(1024), 0, s, a);
+  else
+    launch(MOE_PROF_Q4, q4_rows_kernel<XF32, FP4, MODE, 8>, grid, dim3(512), 0, s, a);
+}
+
+// Whether tiles of 128 rows are worth it.  The few-row form's workgroups take 16 rows of 16
+// matrix rows and run 512 at a time, the tiles' 128 of 128 (SWIGLU 256) and run 256 at a
+// time, each turn as long as thousands of the small ones.  Both measured, 4096 inputs and
+// 4096 outputs, us a turn of tiles (up to 1024 rows) and rows of the small form in that
+// time: MXFP4 33 and 180, other E2M1 36 and 200, integer codes 53 and 265, groups under 128
+// 72 to 104 and 340 to 370, fp32 x 115 to 192 and 340 to 450.  SWIGLU, integer codes, 2048
+// outputs of 64 experts, the small form and tiles: 512 rows 192 and 266, 1024 rows 276 and
+// 278, 2048 rows 442 and 331.
+template <bool XF32, bool FP4>
+bool use_tiles(const Q4Args& a) {
+  if ((uintptr_t)a.x % 16) return false;  // the tiles' direct loads to LDS
+  const int live = std::min(a.num, a.T);
+  const long small = (a.offsets ? a.T / 16 + live / 2 : (a.T + 15) / 16) * (long)((a.N + 15) / 16) * (a.swiglu ? 2 : 1);
+  const long large = (a.offsets ? a.T / 128 + live : (a.T + 127) / 128) * (long)((a.N + 127) / 128);
+  const bool plain = !XF32 && (a.group % 128 == 0 || (FP4 && a.st == MOE_SCALE_E8M0 && a.group == 32));
+  return small > (plain ? (FP4 ? 3000 : 4000) : 6000) * ((large + 255) / 256);
 }
 
 template <bool XF32, bool FP4>
 void run_q4(const Q4Args& a, hipStream_t s) {
-  const int rows = a.offsets ? (a.T + a.num - 1) / a.num : a.T;
-  int lim = getenv("MOE_LIM") ? atoi(getenv("MOE_LIM")) : 64;
-  if (rows > lim && (uintptr_t)a.x % 16 == 0) {
+  if (use_tiles<XF32, FP4>(a)) {
     launch_q4_tile(a, XF32, FP4, s);
     return;
   }

@@ -2,6 +2,7 @@
 // codes' and inputs' ways to bf16, and the search for a row tile's matrix.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "chunk_dev.h"
@@ -71,14 +72,6 @@ template <bool XF32>
 struct XPart {
   static constexpr int kParts = XF32 ? 3 : 1;
   v8bf p[kParts];
-  __device__ __forceinline__ void load(const void* x, size_t at) {
-    if constexpr (!XF32) {
-      const uint4 h = ld8h((const uint16_t*)x + at);
-      p[0] = as_bf(u32x4_t{h.x, h.y, h.z, h.w});
-    } else {
-      split(ld8f((const float*)x + at));
-    }
-  }
   __device__ __forceinline__ void split(f32x8 f) {
     if constexpr (XF32) {
 #pragma unroll
@@ -97,37 +90,12 @@ struct XPart {
   }
 };
 
-// A scale as it is stored, and its value: nothing between the loads of a batch waits for
-// one of them.
-__device__ __forceinline__ uint32_t raw_scale(const void* p, int st, size_t at) {
-  if (st == MOE_F32) return ((const uint32_t*)p)[at];
-  if (st == MOE_BF16) return ((const uint16_t*)p)[at];
-  return ((const uint8_t*)p)[at];
-}
-
 __device__ __forceinline__ float scale_of(uint32_t raw, int st) {
   return st == MOE_F32 ? __uint_as_float(raw) : st == MOE_BF16 ? __uint_as_float(raw << 16) : e8m0_to_f32(raw);
 }
 
 // The group of the inputs from 32 c on.
 __device__ __forceinline__ int group_of(const Q4Args& a, int c) { return (int)__umulhi((uint32_t)c, a.magic) + c * a.unit; }
-
-// Four lanes that hold a row's chunks (lane 16 q + c: chunk q, dword j in d[j]) exchange
-// them so that d[j] is dword q of chunk j.
-__device__ __forceinline__ void transpose4(uint32_t (&d)[4]) {
-  auto swap16 = [](uint32_t& a, uint32_t& b) {
-    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-    a = r[0], b = r[1];
-  };
-  auto swap32 = [](uint32_t& a, uint32_t& b) {
-    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    a = r[0], b = r[1];
-  };
-  swap16(d[0], d[1]);
-  swap16(d[2], d[3]);
-  swap32(d[0], d[2]);
-  swap32(d[1], d[3]);
-}
 
 // sum of the lanes up to this one
 __device__ __forceinline__ int wave_scan(int v) {
@@ -145,6 +113,11 @@ __device__ __forceinline__ int wave_scan(int v) {
 struct Tile {
   int e, row, rows;
 };
+
+// Row tiles of a launch: a matrix's last may be short, one at most for each that has rows.
+inline int tile_groups(const Q4Args& a, int size) {
+  return a.offsets ? a.T / size + std::min(a.num, a.T) : (a.T + size - 1) / size;
+}
 
 // LARGE: tiles of more than half the size come first, so that the chip does not end on
 // them alone.

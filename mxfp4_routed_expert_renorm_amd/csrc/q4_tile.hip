@@ -422,14 +422,23 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
 template <bool XF32, bool FP4, int MODE, int NT>
 void run(const Q4Args& a, hipStream_t s) {
   const int cols = a.swiglu ? 128 : 128 * NT;
-  const int tiles = a.offsets ? a.T / kRows + min(a.num, a.T) : (a.T + kRows - 1) / kRows;
+  const int tiles = tile_groups(a, kRows);
   const dim3 grid((a.N + cols - 1) / cols, min(tiles, kTilesY), (tiles + kTilesY - 1) / kTilesY);
   launch(MOE_PROF_Q4, q4_tile_kernel<XF32, FP4, MODE, NT>, grid, dim3(512), 0, s, a);
 }
 
 template <bool XF32, bool FP4, int MODE>
 void run_shape(const Q4Args& a, hipStream_t s) {
-  run<XF32, FP4, MODE, 2>(a, s);
+  // A workgroup of 256 matrix rows takes 1.65 times one of 128 (4096 inputs, integer codes 89
+  // and 53 us, MXFP4 50 and 33), so that the smaller one wins where it fills turns of the
+  // chip that the larger would not: 1024 rows by 4096 MXFP4 37 us against 53; 2048 rows of
+  // integer codes are one turn of the larger, 95 us, or two of the smaller.  SWIGLU has 32 gate
+  // and 32 up rows in a wavefront and takes the larger.
+  const long tiles = tile_groups(a, kRows), w1 = tiles * ((a.N + 127) / 128), w2 = tiles * ((a.N + 255) / 256);
+  if (a.swiglu || 1.65 * ((w2 + 255) / 256) < (double)((w1 + 255) / 256))
+    run<XF32, FP4, MODE, 2>(a, s);
+  else
+    run<XF32, FP4, MODE, 1>(a, s);
 }
 
 template <bool XF32, bool FP4>
