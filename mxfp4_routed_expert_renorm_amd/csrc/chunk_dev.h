@@ -61,6 +61,17 @@ __device__ __forceinline__ f32x8 widen(uint4 h) {
                bf16_lo(h.z), bf16_hi(h.z), bf16_lo(h.w), bf16_hi(h.w)};
 }
 
+// sum of the lanes up to this one
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, dpp::kRowBcast15, 0xa, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, dpp::kRowBcast31, 0xc, 0xf, false);
+  return v;
+}
+
 // fp32 -> bf16, to nearest even, NaN stays NaN: one instruction for two.  With
 // the rounding in integer steps the norms, though bound by memory, took 13.3
 // instead of 12.2 us and 28.9 instead of 27.4 (4096 x 4096).

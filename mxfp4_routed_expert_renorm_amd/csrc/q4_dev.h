@@ -97,17 +97,6 @@ __device__ __forceinline__ float scale_of(uint32_t raw, int st) {
 // The group of the inputs from 32 c on.
 __device__ __forceinline__ int group_of(const Q4Args& a, int c) { return (int)__umulhi((uint32_t)c, a.magic) + c * a.unit; }
 
-// sum of the lanes up to this one
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1, 2, 4, 8
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, dpp::kRowBcast15, 0xa, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, dpp::kRowBcast31, 0xc, 0xf, false);
-  return v;
-}
-
 // The matrix and the rows of the row tile that a workgroup takes, of `size` rows each but
 // for a matrix's last.  False: there is none.
 struct Tile {
