@@ -48,6 +48,11 @@ __device__ __forceinline__ f32x8 ld8f(const float* p) {
   return f32x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
+__device__ __forceinline__ uint4 ld4w(const uint32_t* p) {
+  const Packed4f v = *(const Packed4f*)p;
+  return make_uint4(__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w));
+}
+
 __device__ __forceinline__ float ld1f_if(const float* p, bool there) { return there ? *p : 0.0f; }
 
 __device__ __forceinline__ f32x8 ld8f_to(const float* p, int n) {
