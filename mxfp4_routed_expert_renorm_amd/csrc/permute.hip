@@ -42,6 +42,8 @@ struct PermuteArgs {
   int T, k, H, E;
 };
 
+typedef uint32_t u32x4_word __attribute__((ext_vector_type(4), aligned(4)));
+
 // 16 bytes of a row as they are: a NaN keeps its payload
 template <bool BF16>
 struct Chunk {
@@ -74,7 +76,7 @@ struct Chunk {
     } else {
       uint32_t* o = (uint32_t*)xs + row + c.at;
       if (c.n == 4) {
-        stream4f((float*)o, f32x4{__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)});
+        __builtin_nontemporal_store(u32x4_word{v.x, v.y, v.z, v.w}, (u32x4_word*)o);
       } else {
 #pragma unroll
         for (int j = 0; j < 3; ++j)
@@ -100,9 +102,10 @@ __device__ __forceinline__ int group_scan(int v, int* part, int& total) {
   return before + up_to - v;
 }
 
-// Few pairs, one launch (64 tokens x 8 of 4096 bf16: 4.2 us, of which the launch is 1.9): a workgroup finds its token's places by itself, pair p of expert
-// e standing behind the pairs q with (ids[q], q) < (e, p), and writes the token's row there.
+// Few pairs, one launch: a workgroup finds its token's places by itself, pair p of expert e
+// standing behind the pairs q with (ids[q], q) < (e, p), and writes the token's row there.
 // Workgroup 0 counts the experts' pairs.  An id outside [0, E) is above all as unsigned.
+// 64 tokens x 8 of 4096 bf16: 4.2 us, of which the launch is 1.9.
 template <bool BF16>
 __global__ __launch_bounds__(256) void permute_few_kernel(PermuteArgs a) {
   const int P = a.T * a.k, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -453,8 +456,8 @@ moe_status launch_permute(const void* x, moe_dtype xt, int T, int k, int H, int 
   const bool bf16 = xt == MOE_BF16;
   if (T * k <= kFewPairs) {
     const int wide = bf16 ? 2048 : 1024, segs = xs ? min((H + wide - 1) / wide, max(1, 1024 / max(T, 1))) : 1;
-    launch(MOE_PROF_PERMUTE, bf16 ? permute_few_kernel<true> : permute_few_kernel<false>, dim3(T + 1, segs), dim3(256), 0,
-           s, a);
+    auto f = bf16 ? permute_few_kernel<true> : permute_few_kernel<false>;
+    launch(MOE_PROF_PERMUTE, f, dim3(T + 1, segs), dim3(256), 0, s, a);
   } else {
     const int tokens = chunk_tokens(T), chunks = (T + tokens - 1) / tokens;
     int bits = 0;
@@ -462,8 +465,8 @@ moe_status launch_permute(const void* x, moe_dtype xt, int T, int k, int H, int 
     launch(MOE_PROF_PERMUTE, permute_count_kernel, dim3(chunks), dim3(256), 0, s, ids, T * k, E, tokens * k, scratch);
     MOE_LAUNCH_CHECK();
     const size_t lds = (size_t)(kRankWaves * E + tokens * k) * sizeof(int);
-    launch(MOE_PROF_PERMUTE, bf16 ? permute_place_kernel<true> : permute_place_kernel<false>, dim3(chunks), dim3(1024), lds,
-           s, a, tokens, bits, (const int32_t*)scratch);
+    auto f = bf16 ? permute_place_kernel<true> : permute_place_kernel<false>;
+    launch(MOE_PROF_PERMUTE, f, dim3(chunks), dim3(1024), lds, s, a, tokens, bits, (const int32_t*)scratch);
   }
   MOE_LAUNCH_CHECK();
   return MOE_OK;

@@ -95,7 +95,9 @@ __device__ __forceinline__ float scale_of(uint32_t raw, int st) {
 }
 
 // The group of the inputs from 32 c on.
-__device__ __forceinline__ int group_of(const Q4Args& a, int c) { return (int)__umulhi((uint32_t)c, a.magic) + c * a.unit; }
+__device__ __forceinline__ int group_of(const Q4Args& a, int c) {
+  return (int)__umulhi((uint32_t)c, a.magic) + c * a.unit;
+}
 
 // The matrix and the rows of the row tile that a workgroup takes, of `size` rows each but
 // for a matrix's last.  False: there is none.

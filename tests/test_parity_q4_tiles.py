@@ -44,8 +44,8 @@ def test_q4_linear_rows_of_x_anywhere(gpu_lib, shift, xt, code, scale, zeros):
     _close(_f64(y.check()), *w.product(_f64(x), 0, "bf16"), f"x off by {shift}")
 
 
-@pytest.mark.parametrize("counts", [[700, 0, 1, 129, 500, 3], [64, 65] * 12, [0, 1400, 0], [0] * 66 + [1300, 1, 127, 128]],
-                         ids=lambda c: f"{len(c)}m{sum(c)}r")
+@pytest.mark.parametrize("counts", [[700, 0, 1, 129, 500, 3], [64, 65] * 12, [0, 1400, 0],
+                                    [0] * 66 + [1300, 1, 127, 128]], ids=lambda c: f"{len(c)}m{sum(c)}r")
 @pytest.mark.parametrize("xt,yt", [("bf16", "bf16"), ("f32", "f32")])
 @pytest.mark.parametrize("code,scale", [("int4", "bf16"), ("fp4", "e8m0"), ("fp4", "f32")])
 def test_q4_grouped_tiles(gpu_lib, counts, xt, yt, code, scale):
@@ -87,7 +87,8 @@ def test_q4_few_rows_of_a_long_matrix(gpu_lib, xt, code, scale, zeros):
         gpu_lib.moe_q4_linear(w.q4, x, y.t)
         torch.cuda.synchronize()
         _close(_f64(y.check()), *w.product(_f64(x), 0, "f32"), f"{T} x {N} x {K}")
-    _grouped(gpu_lib, rng, Weights(gpu_lib, rng, 30, 160, 1024, 256, code, scale, zeros, "swiglu"), [1, 0, 20] * 10, xt, "f32")
+    w = Weights(gpu_lib, rng, 30, 160, 1024, 256, code, scale, zeros, "swiglu")
+    _grouped(gpu_lib, rng, w, [1, 0, 20] * 10, xt, "f32")
 
 
 @pytest.mark.parametrize("T", [128, 3328])
