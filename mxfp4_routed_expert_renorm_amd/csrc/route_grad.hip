@@ -8,6 +8,9 @@
 //
 // One wavefront per token: lane i holds pick i, and expert 4 (lane + 64 j) + i is
 // element i of a lane's vector j, so that a row leaves in 16-byte stores.
+//
+// Bound by the launch and a token's chain of loads, reductions and stores: 4096 tokens of
+// 256 experts 4.6 us, 777 of 300, every expert's gradient, 4.8 (1.9 a launch alone).
 #include "chunk_dev.h"
 
 namespace moe {
