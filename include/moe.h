@@ -333,10 +333,11 @@ moe_status moe_route_grad(const moe_router* router, const void* logits, moe_dtyp
  *   MOE_Q4_LINEAR: y as above;  MOE_Q4_SWIGLU: the matrix has 2 N rows, gate above up,
  *   and y[t][n] = silu(gate) * up
  * Two codes per byte, input 2j in the low nibble.  A group's sum of v * x is formed in
- * fp32 from exact products (fp32 x keeps all its bits), then scaled and added in fp32
- * (E2M1 codes with E8M0 scales for groups of 32 are scaled first, which is exact but for
- * weights beyond fp32's range: they are infinite); y is rounded once.  An infinity or NaN in a row of x leaves that row of y infinite or
- * NaN, and no other row.
+ * fp32 from exact products (fp32 x keeps its bits down to 2^-133; of integer codes it may
+ * be sum code * x - zero * sum x), then scaled and added in fp32; E2M1 codes with E8M0
+ * scales for groups of 32 are scaled first, which is exact but for weights beyond fp32's
+ * range: they are infinite.  y is rounded once.  An infinity or NaN in a row of x leaves
+ * that row of y infinite or NaN, and no other row.
  * An expert record (see above) holds two such matrices: w1 and w3 with their scales
  * stand together as a SWIGLU matrix of I outputs, w2 as a LINEAR one of H. */
 enum { MOE_Q4_INT4 = 0, MOE_Q4_FP4 = 1 };
