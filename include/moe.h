@@ -331,7 +331,7 @@ moe_status moe_route_grad(const moe_router* router, const void* logits, moe_dtyp
  *   MOE_Q4_INT4: v = code - zero[n][i / group], codes 0..15, zeros NULL: 8
  *   MOE_Q4_FP4:  v = the E2M1 value (sign, 2-bit exponent, mantissa), as the expert records'
  *   MOE_Q4_LINEAR: y as above;  MOE_Q4_SWIGLU: the matrix has 2 N rows, gate above up,
- *   and y[t][n] = silu(gate) * up
+ *   and y[t][n] = silu(gate) * up, silu(v) = v * sigmoid(v); a sigmoid below 2^-126 counts as 0
  * Two codes per byte, input 2j in the low nibble.  A group's sum of v * x is formed in
  * fp32 from exact products (fp32 x keeps its bits down to 2^-133; of integer codes it may
  * be sum code * x - zero * sum x), then scaled and added in fp32; E2M1 codes with E8M0

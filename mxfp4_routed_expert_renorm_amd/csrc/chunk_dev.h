@@ -168,16 +168,18 @@ __device__ __forceinline__ float load1(const void* p, bool bf16, size_t at) {
 // step of fp32, the argument's rounding growing with |g|
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
-// 1 / (1 + e^-g) within 8 roundings (2^-24) of its value wherever g lies.  e^-g is
-// 2^t, t = -g log2(e); what rounding took from t comes back as a factor 1 + rest ln(2),
-// or the error would grow with |g|, to some |g| roundings.  The hardware's power of 2
-// and reciprocal are each within a step.  moe_norm_out, 4096 x 4096 bf16, a gate
-// per element 32.0 -> 32.8 us; with the library's expf 33.4.
+// 1 / (1 + e^-g) within 8 roundings (2^-24) of its value wherever g lies, 0 where that is
+// below 2^-126.  e^-g is 2^t, t = -g log2(e); what rounding took from t comes back as a
+// factor 1 + rest ln(2), or the error would grow with |g|, to some |g| roundings.  From
+// 2^128 on the power is infinite and takes no factor: infinity times a rest of 0, or with
+// one below 0 added to itself, is NaN.  The hardware's power of 2 and reciprocal are each
+// within a step.  moe_norm_out, 4096 x 4096 bf16, a gate per element 32.0 -> 32.8 us; with
+// the library's expf 33.4.
 __device__ __forceinline__ float gate_sigmoid(float g) {
   constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 1.925963e-8f, kLn2 = 0.6931472f;  // log2(e) in two parts
   const float t = -kLog2e * g, p = __builtin_amdgcn_exp2f(t);
   const float rest = fmaf(-kLog2eRest, g, fmaf(-kLog2e, g, -t));
-  const float e = fabsf(t) < 150.0f ? fmaf(p, rest * kLn2, p) : p;  // beyond, 0 or infinity (and NaN) as they are
+  const float e = fabsf(t) < 128.0f ? fmaf(p, rest * kLn2, p) : p;  // beyond, 1 + e is 1 or infinite, or g is NaN
   return __builtin_amdgcn_rcpf(1.0f + e);
 }
 

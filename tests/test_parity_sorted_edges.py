@@ -1,0 +1,93 @@
+"""GPU parity of the calls around rows sorted by expert where values or sizes are at an end,
+against float64.
+
+u = 2^-24 is half a step of fp32.  A sigmoid is within 8 u of its value, and 0 may stand for
+one below 2^-126."""
+import numpy as np
+import pytest
+
+from tests.test_parity_block import U, Guarded, _close, _dt, _f64, _torch, _up
+from tests.test_parity_sorted import _i32, _route_grad_tol
+from oracle import sorted_oracle as S
+
+pytestmark = pytest.mark.gpu
+
+TINY = 2.0 ** -126
+
+
+# ------------------------------------------------------------------- saturated sigmoids
+
+def _saturated():
+    """Gates around the places where e^-g passes fp32's range (88.7) and where it leaves the
+    correction's (104), both ends and what lies between."""
+    return np.concatenate([np.linspace(-110, -80, 481), np.linspace(80, 110, 61), [0.0]])
+
+
+@pytest.mark.parametrize("kind", ["channel", "token", "full"])
+@pytest.mark.parametrize("gt", ["f32", "bf16"])
+def test_norm_out_saturated_gates(gpu_lib, kind, gt):
+    """alpha, the product with y and the sum with a residual of 0 round once each: 11 u."""
+    torch = _torch()
+    g = _saturated()
+    T, H = (len(g), 40) if kind == "token" else (7, len(g))
+    gate = _up(np.tile(g, (T, 1)) if kind == "full" else g, gt)
+    y, res = _up(np.random.default_rng(0).uniform(0.5, 2.0, (T, H)), "f32"), torch.zeros(T, H, device="cuda")
+    out = Guarded((T, H), "f32")
+    gpu_lib.moe_norm_out(gpu_lib.make_norm(H, gate=kind, gate_act="sigmoid", alpha=0.75), y, res, gate, out.t)
+    torch.cuda.synchronize()
+    g = _f64(gate)
+    ref = 0.75 * _f64(y) / (1.0 + np.exp(-(g[:, None] if kind == "token" else g)))
+    _close(_f64(out.check()), ref, 11 * U * ref + 2 * TINY, kind)
+
+
+@pytest.mark.parametrize("rows", ["few", "tile"])
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("code", ["int4", "fp4"])
+@pytest.mark.parametrize("group", [32, 128])
+def test_q4_swiglu_saturated_gates(gpu_lib, rows, xt, code, group):
+    """Matrices that pass a gate and an up value through: the sums are exact, so the error is
+    the sigmoid's 8 u and that of two products, 10 u; a sigmoid taken as 0 leaves gate * up of 2^-126."""
+    torch = _torch()
+    rng = np.random.default_rng(0)
+    K, N = 256, 10 if rows == "few" else 750
+    one = 1 if code == "int4" else 2
+    codes = np.zeros((2 * N, K // 2), np.uint8)
+    codes[:N, 0], codes[N:, 0] = one, one << 4  # gate: input 0, up: input 1
+    scales = torch.ones(2 * N, K // group, device="cuda")
+    zeros = torch.zeros(2 * N, K // group, dtype=torch.uint8, device="cuda") if code == "int4" else None
+    scales = torch.full_like(scales, 127, dtype=torch.uint8) if code == "fp4" and group == 32 else scales
+    q4 = gpu_lib.make_q4(torch.from_numpy(codes).cuda(), scales, zeros, code=code, act="swiglu")
+    g = _saturated()
+    for part in [g[i:i + 16] for i in range(0, len(g), 16)] if rows == "few" else [np.tile(g, 3)]:
+        x = np.zeros((len(part), K))
+        x[:, 0], x[:, 1] = part, rng.uniform(-1, 1, len(part))
+        x, y = _up(x, xt), Guarded((len(part), N), "f32")
+        gpu_lib.moe_q4_linear(q4, x, y.t)
+        torch.cuda.synchronize()
+        gate, up = _f64(x)[:, :1], _f64(x)[:, 1:2]
+        ref = gate / (1 + np.exp(-gate)) * up
+        _close(_f64(y.check()), np.tile(ref, (1, N)), 10 * U * np.abs(ref) + 2 * TINY * np.abs(gate * up) + TINY,
+               f"gates from {part[0]}")
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("lt", ["bf16", "f32"])
+def test_route_grad_saturated_logits(gpu_lib, renorm, lt):
+    """Picked logits where 1 - s leaves fp32's range."""
+    torch = _torch()
+    rng = np.random.default_rng(1)
+    top = _saturated()
+    T, E, k = len(top), 70, 4
+    lg = rng.standard_normal((T, E))
+    lg[:, 3] = top
+    ids = np.tile(np.array([3, 9, 40, 69]), (T, 1))
+    lg = _up(lg, lt)
+    s = S.scores(_f64(lg)[np.arange(T)[:, None], ids], "sigmoid")
+    w = _up(s / s.sum(1, keepdims=True) if renorm else s, "f32")
+    g, out = _up(rng.standard_normal((T, k)), "f32"), Guarded((T, E), "f32")
+    gpu_lib.moe_route_grad(gpu_lib.make_router(E, k, scoring="sigmoid", renorm=renorm), lg, _i32(ids), w, g, out.t)
+    torch.cuda.synchronize()
+    args = (_f64(lg), ids, _f64(w), _f64(g), "sigmoid", renorm)
+    ref, mag = S.route_grad(*args)
+    far = 2 * TINY * np.abs(_f64(w)).max() * 2 * np.abs(_f64(g)).max()
+    _close(_f64(out.check()), ref, _route_grad_tol(*args, ref, mag, _dt("f32")) + far, "saturated")
