@@ -226,14 +226,20 @@ struct TileKernel {
       return x;
     };
 
-    // chunks: of 32 inputs, that the stage holds
+    // chunks: of 32 inputs, that the stage holds (four and more if it is whole)
     auto multiply = [&](auto nm, auto whole, int stage, int buf, int chunks) {
       constexpr int NM = decltype(nm)::value;
       constexpr bool kWhole = decltype(whole)::value;
       uint32_t bytes[NT];
       if constexpr (kFolded) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) bytes[i] = bytes_at(stage, buf, i) >> (8 * h);
+        for (int i = 0; i < NT; ++i) {
+          bytes[i] = bytes_at(stage, buf, i);
+          // The bytes past the row's end are another row's, or nobody's: as 255, 254 or 253 they
+          // would make weights that x of 0 does not take away.
+          if (!kWhole) bytes[i] &= (1u << (8 * chunks)) - 1;
+          bytes[i] >>= 8 * h;
+        }
       }
       v16f part[NM][NT];  // of the stage
       if constexpr (MODE == kStage) {

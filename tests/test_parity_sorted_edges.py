@@ -91,3 +91,43 @@ def test_route_grad_saturated_logits(gpu_lib, renorm, lt):
     ref, mag = S.route_grad(*args)
     far = 2 * TINY * np.abs(_f64(w)).max() * 2 * np.abs(_f64(g)).max()
     _close(_f64(out.check()), ref, _route_grad_tol(*args, ref, mag, _dt("f32")) + far, "saturated")
+
+
+# ------------------------------------------------------------------- scales that are not a row's own
+
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("K", [96, 160, 224, 416, 1184])
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("xt,few", [("bf16", False), ("bf16", True), ("f32", False)])
+def test_q4_reads_no_scale_but_a_row_s_own(gpu_lib, xt, few, grouped, K, act):
+    """MXFP4, an odd number of groups a row, so that rows end inside a stage: every row's
+    result is the same whatever the other rows' scales are and what lies behind the last."""
+    torch = _torch()
+    rng = np.random.default_rng(K)
+    num, N, T = (3, 751, 1500) if grouped else (1, 1301 if act == "none" else 751, 1300)
+    T = 37 if few else T
+    R, G = N * (2 if act == "swiglu" else 1), K // 32
+    codes = torch.from_numpy(rng.integers(0, 256, (num, R, K // 2), dtype=np.uint8)).cuda()
+    good = torch.from_numpy(rng.integers(117, 126, (num, R, G), dtype=np.uint8)).cuda()
+    x = _up(rng.standard_normal((T, K)) / K ** 0.5, xt)
+    offsets = _i32([0, T // 2, T // 2 + 1, T])
+
+    def product(scales):
+        y = Guarded((T, N), "f32")
+        q4 = gpu_lib.make_q4(codes, scales, code="fp4", act=act)
+        gpu_lib.moe_q4_grouped(q4, x, offsets, y.t) if grouped else gpu_lib.moe_q4_linear(q4, x, y.t)
+        return y.check()
+    want = product(good)
+    assert bool(want.isfinite().all())
+    for byte in (255, 254, 253):
+        # behind the last: a view of a longer buffer; at every place that a word's bytes can have
+        for shift in range(4):
+            far = torch.full((shift + good.numel() + 64,), byte, dtype=torch.uint8, device="cuda")
+            view = far[shift:shift + good.numel()].view(good.shape)
+            view.copy_(good)
+            assert torch.equal(product(view), want), f"{byte} behind the last scale, {shift}"
+        for odd in (0, 1):  # every second output's rows, gate and up alike
+            other = good.clone().view(num, -1, N, G)
+            other[:, :, odd::2] = byte
+            got = product(other.view(good.shape))
+            assert torch.equal(got[:, 1 - odd::2], want[:, 1 - odd::2]), f"{byte} in the rows between"
