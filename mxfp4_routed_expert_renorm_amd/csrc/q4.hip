@@ -343,21 +343,16 @@ bool use_tiles(const Q4Args& a) {
 }
 
 template <bool XF32, bool FP4>
-void run_q4(const Q4Args& a, hipStream_t s) {
-  if (use_tiles<XF32, FP4>(a)) {
-    launch_q4_tile(a, XF32, FP4, s);
-    return;
-  }
-  if constexpr (FP4) {
-    if (a.st == MOE_SCALE_E8M0 && a.group == 32 && a.K >= 128) {
-      run_rows<XF32, FP4, kFold>(a, s);
-      return;
-    }
-  }
-  if (a.group % 128 == 0)
+moe_status run_q4(const Q4Args& a, hipStream_t s) {
+  if (use_tiles<XF32, FP4>(a)) return launch_q4_tile(a, XF32, FP4, s);
+  if (FP4 && a.st == MOE_SCALE_E8M0 && a.group == 32 && a.K >= 128)
+    run_rows<XF32, FP4, FP4 ? kFold : kChunk>(a, s);
+  else if (a.group % 128 == 0)
     run_rows<XF32, FP4, kBlock>(a, s);
   else
     run_rows<XF32, FP4, kChunk>(a, s);
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
 }
 
 }  // namespace
@@ -368,12 +363,8 @@ moe_status launch_q4(const moe_q4* q, const void* x, moe_dtype xt, int T, const 
                  q->act == MOE_Q4_SWIGLU, yt == MOE_BF16, q->code_stride, q->scale_stride, q->zero_stride,
                  q->group == 32 ? 0u : (uint32_t)(((uint64_t)1 << 32) / (q->group / 32)) + 1, q->group == 32};
   const bool xf = xt == MOE_F32, fp4 = q->code == MOE_Q4_FP4;
-  if (xf)
-    fp4 ? run_q4<true, true>(a, s) : run_q4<true, false>(a, s);
-  else
-    fp4 ? run_q4<false, true>(a, s) : run_q4<false, false>(a, s);
-  MOE_LAUNCH_CHECK();
-  return MOE_OK;
+  if (xf) return fp4 ? run_q4<true, true>(a, s) : run_q4<true, false>(a, s);
+  return fp4 ? run_q4<false, true>(a, s) : run_q4<false, false>(a, s);
 }
 
 }  // namespace moe
