@@ -326,7 +326,7 @@ struct UnpermuteArgs {
 // 777 x 6 of 2047 onto an fp32 base 7.1 us, 4.2 TB/s.
 template <bool YBF16, bool OBF16>
 __global__ __launch_bounds__(256) void unpermute_kernel(UnpermuteArgs a) {
-  const int wave = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wave = (blockIdx.y * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int t = __builtin_amdgcn_readfirstlane(wave / a.segs), seg = wave - t * a.segs;
   const int e = (seg * 64 + lane) * 8;
   if (t >= a.T || e >= a.H) return;
@@ -478,7 +478,10 @@ moe_status launch_unpermute(const void* ys, moe_dtype yt, int M, const int32_t* 
   const bool yb = yt == MOE_BF16, ob = ot == MOE_BF16;
   auto f = yb ? (ob ? unpermute_kernel<true, true> : unpermute_kernel<true, false>)
               : (ob ? unpermute_kernel<false, true> : unpermute_kernel<false, false>);
-  launch(MOE_PROF_PERMUTE, f, dim3((unsigned)(((size_t)T * a.segs + 3) / 4)), dim3(256), 0, s, a);
+  // a dimension of a launch has fewer than 2^32 threads, and the largest sizes need 2^33
+  constexpr int kAcross = 1 << 22;
+  const int groups = (int)(((size_t)T * a.segs + 3) / 4);
+  launch(MOE_PROF_PERMUTE, f, dim3(min(groups, kAcross), (groups + kAcross - 1) / kAcross), dim3(256), 0, s, a);
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }

@@ -88,3 +88,7 @@ def _child(tmp_path, fails):
 
 def test_failed_launches_are_reported(tmp_path):
     _child(tmp_path, 1)
+
+
+def test_launches_fit_the_device_up_to_the_largest_sizes(tmp_path):
+    _child(tmp_path, 0)

@@ -131,3 +131,22 @@ def test_q4_reads_no_scale_but_a_row_s_own(gpu_lib, xt, few, grouped, K, act):
             other[:, :, odd::2] = byte
             got = product(other.view(good.shape))
             assert torch.equal(got[:, 1 - odd::2], want[:, 1 - odd::2]), f"{byte} in the rows between"
+
+
+# ------------------------------------------------------------------- the largest sizes
+
+@pytest.mark.parametrize("T,H", [(1 << 20, 32768 - 8), (5, 65536)])
+def test_unpermute_largest(gpu_lib, T, H):
+    """Up to 2^32 threads' worth of rows: few rows of ys, found from every token."""
+    torch = _torch()
+    M = 3
+    ys = torch.randn(M, H, device="cuda").bfloat16()
+    rows = (torch.arange(T, dtype=torch.int32, device="cuda") % (M + 1) - 1).view(T, 1)  # every fourth dropped
+    out = torch.full((T * H + 8,), 77, dtype=torch.bfloat16, device="cuda")
+    gpu_lib.moe_unpermute(ys, rows, None, None, out[:T * H].view(T, H))
+    want = torch.cat([torch.zeros_like(ys[:1]), ys])
+    at = out[:T * H].view(T, H)
+    for t0 in range(0, T, 1 << 14):
+        part = at[t0:t0 + (1 << 14)]
+        assert torch.equal(part, want[torch.arange(t0, t0 + len(part), device="cuda") % (M + 1)]), t0
+    assert bool((out[T * H:] == 77).all())
