@@ -150,3 +150,44 @@ def test_unpermute_largest(gpu_lib, T, H):
         part = at[t0:t0 + (1 << 14)]
         assert torch.equal(part, want[torch.arange(t0, t0 + len(part), device="cuda") % (M + 1)]), t0
     assert bool((out[T * H:] == 77).all())
+
+
+# ------------------------------------------------------------------- a confident router's gradient
+
+@pytest.mark.parametrize("E,k,T", [(2, 1, 5), (8, 2, 9), (70, 1, 12), (256, 8, 40), (300, 6, 33), (1000, 8, 12),
+                                   (1024, 64, 5)])
+@pytest.mark.parametrize("lt", ["f32", "bf16"])
+def test_route_grad_of_a_confident_router(gpu_lib, E, k, T, lt):
+    """Softmax weights that are not renormalised, one expert far above the rest: its gradient
+    w g (1 - s) - s (the other picks' g w) has all its digits, not those of w g alone.
+
+    Each exponential carries |x - top| roundings of its argument and 4 more, the sum of the
+    others at most E/64 + 16, quotient and result fewer than 8; the picks' part is formed in double."""
+    torch = _torch()
+    rng = np.random.default_rng(E + k)
+    lg = rng.standard_normal((T, E))
+    lead = rng.integers(0, E, T)
+    gap = np.resize([0.0, 6.0, 12.0, 15.0, 18.0, 25.0, 40.0, 80.0], T)
+    lg[np.arange(T), lead] = lg.max(1) + gap
+    lg = _up(lg, lt)
+    x = _f64(lg)
+    ids = np.argsort(-x, axis=1, kind="stable")[:, :k].astype(np.int32)
+    if k > 4:
+        ids[T // 2, 2:4] = ids[T // 2, 0]  # the leader picked three times
+        ids[T // 3, 1] = -1
+    ex = np.exp(x - x.max(1, keepdims=True))
+    total = ex.sum(1, keepdims=True)
+    w = _up(np.take_along_axis(ex / total, np.maximum(ids, 0), 1), "f32")
+    g, out = _up(rng.standard_normal((T, k)), "f32"), Guarded((T, E), "f32")
+    gpu_lib.moe_route_grad(gpu_lib.make_router(E, k, scoring="softmax", renorm=False), lg, _i32(ids), w, g, out.t)
+    torch.cuda.synchronize()
+    gw = np.where(ids >= 0, _f64(g) * _f64(w), 0.0)
+    ref, mag = np.zeros((T, E)), np.zeros((T, E))
+    for t, e in np.ndindex(T, E):
+        mine = ids[t] == e
+        away = np.delete(ex[t], e).sum() / total[t, 0]  # 1 - s, by its own terms
+        s = ex[t, e] / total[t, 0]
+        ref[t, e] = gw[t, mine].sum() * away - s * gw[t, ~mine].sum()
+        mag[t, e] = np.abs(gw[t, mine]).sum() * away + s * np.abs(gw[t, ~mine]).sum()
+    far = (x.max(1) - x.min(1))[:, None]
+    _close(_f64(out.check()), ref, (far + E / 64 + 16 + 12) * U * mag + TINY, "confident")
