@@ -387,8 +387,13 @@ struct TileKernel {
         }
         buf = buf == kRing - 1 ? 0 : buf + 1;
       };
-      for (int s = 0; s < whole; ++s) stage(std::true_type{}, s);
-      if (whole < stages) stage(std::false_type{}, whole);
+      // Rows end inside a stage only where a stage's groups may: kChunk counts its own, and
+      // kFold2 takes the last stage by itself.  The same for kStage would be dead code that
+      // spilled registers.
+      for (int s = 0; s < (MODE == kFold2 ? whole : stages); ++s) stage(std::true_type{}, s);
+      if constexpr (MODE == kFold2) {
+        if (whole < stages) stage(std::false_type{}, whole);
+      }
     };
     if (blocks == 2)
       go(std::integral_constant<int, 2>{});
