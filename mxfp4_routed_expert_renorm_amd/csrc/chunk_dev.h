@@ -164,6 +164,8 @@ __device__ __forceinline__ float load1(const void* p, bool bf16, size_t at) {
   return bf16 ? bf(((const uint16_t*)p)[at]) : ((const float*)p)[at];
 }
 
+constexpr float kLowestLogit = -0x1.fep127f;  // bf16's lowest value: a logit there or below masks its expert
+
 // 1 / (1 + e^-g): the hardware's exponential of 2 and reciprocal, each within a
 // step of fp32, the argument's rounding growing with |g|
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }

@@ -17,8 +17,6 @@ namespace moe {
 
 namespace {
 
-constexpr float kLowestLogit = -0x1.fep127f;  // bf16's lowest value: a logit there or below masks its expert
-
 struct RouteGradArgs {
   const void* logits;
   const int32_t* ids;

@@ -42,7 +42,6 @@ constexpr uint32_t kMasked = 0x000fffffu;  // high word of -inf's image
 // them are told apart beyond twice that; sums of two, rounded once more, beyond
 // 5.4e-6.
 constexpr float kMaxBias = 8.0f, kApart = 2e-6f, kGroupsApart = 8e-6f;
-constexpr float kLowest = -0x1.fep127f;  // bf16's lowest value: a logit there or below masks its expert
 
 __device__ __forceinline__ double make_f64(uint32_t lo, uint32_t hi) {
   return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
@@ -186,7 +185,7 @@ __device__ __forceinline__ void write_picks(const moe_router& R, uint64_t picks,
 
 // a softmax's exponential in double precision; a masked expert's is 0 (NaN too)
 __device__ __forceinline__ double soft_exp(float l, float top) {
-  return !(l > kLowest) ? 0.0 : l == top ? 1.0 : exp((double)l - (double)top);
+  return !(l > kLowestLogit) ? 0.0 : l == top ? 1.0 : exp((double)l - (double)top);
 }
 
 template <int EPL>
@@ -221,12 +220,12 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
   int32_t* my_ids = ids + (size_t)t * R.k;
   float* my_w = w + (size_t)t * R.k;
 
-  if (sigmoid_scores || (!bias && top > kLowest && top < INFINITY)) {
+  if (sigmoid_scores || (!bias && top > kLowestLogit && top < INFINITY)) {
     float c[EPL];
     bool wide = false;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      const bool live = l[j] > kLowest;
+      const bool live = l[j] > kLowestLogit;
       if (sigmoid_scores) {
         c[j] = sigmoid(l[j]) + b[j];
         wide |= live && fabsf(b[j]) > kMaxBias;
@@ -245,7 +244,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
         // scores, but scores also tie where logits differ by less than a double exponential shows.
         float v[EPL];
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) v[j] = l[j] > kLowest ? l[j] : -INFINITY;
+        for (int j = 0; j < EPL; ++j) v[j] = l[j] > kLowestLogit ? l[j] : -INFINITY;
         stay = best_groups<float, EPL>(R, v, (float*)choice[wave], &last, &apart, &near);
         sure = last > top - 700.f && (apart == 0.f ? !near : apart > kApart);
       } else {
@@ -310,7 +309,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
   double s[EPL], c[EPL];
   if (sigmoid_scores) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) s[j] = l[j] > kLowest ? 1.0 / (1.0 + exp(-(double)l[j])) : 0.0;  // NaN: 0
+    for (int j = 0; j < EPL; ++j) s[j] = l[j] > kLowestLogit ? 1.0 / (1.0 + exp(-(double)l[j])) : 0.0;  // NaN: 0
   } else {
     double sum = 0.0;
 #pragma unroll
@@ -325,7 +324,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_groups_kernel(moe_router R,
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     c[j] = s[j] + (double)b[j];
-    const bool live = l[j] > kLowest && c[j] > -inf;
+    const bool live = l[j] > kLowestLogit && c[j] > -inf;
     c[j] = live ? c[j] + 0.0 : -inf;  // -0 becomes 0
     s[j] = live ? s[j] : 0.0;
   }
