@@ -313,6 +313,8 @@ moe_status moe_unpermute_grad(const void* gout, moe_dtype gt, const void* ys, mo
  *     sigmoid            d[pick] = w (1 - s[pick]) (g - m)
  *     softmax, renorm    d[pick] = w (g - m)
  *     softmax            d[e]    = sum over picks of e of g w - s[e] * sum over picks of g w,  every e
+ *                        (at picks with 1 - s[e] from the other experts' scores, so that it has
+ *                        its digits where s[e] is near 1)
  * and 0 for all other experts.  A pick of weight 0 (masked) or outside [0, E) adds
  * nothing, whatever its g; an expert picked twice gets the sum.  Masked logits (as
  * moe_route_groups') have s = 0.
@@ -334,7 +336,8 @@ moe_status moe_route_grad(const moe_router* router, const void* logits, moe_dtyp
  *   and y[t][n] = silu(gate) * up, silu(v) = v * sigmoid(v); a sigmoid below 2^-126 counts as 0
  * Two codes per byte, input 2j in the low nibble.  A group's sum of v * x is formed in
  * fp32 from exact products (fp32 x keeps its bits down to 2^-133; of integer codes it may
- * be sum code * x - zero * sum x), then scaled and added in fp32; E2M1 codes with E8M0
+ * be sum code * x - zero * sum x, whose parts pass fp32's range before their difference
+ * does), then scaled and added in fp32; E2M1 codes with E8M0
  * scales for groups of 32 are scaled first, which is exact but for weights beyond fp32's
  * range: they are infinite.  y is rounded once.  An infinity or NaN in a row of x leaves
  * that row of y infinite or NaN, and no other row.
@@ -358,7 +361,9 @@ typedef struct {
 } moe_q4;
 
 /* y[t] = W[0] x[t]: x [T][K] in xt, y [T][N] in yt, overlapping no input.
- * 0 <= T <= 2^20.  Pointers aligned to their element. */
+ * 0 <= T <= 2^20.  Pointers aligned to their element.  Many rows are fast (matrix tiles)
+ * only where x starts at a multiple of 16 bytes; elsewhere 1024 of them take about four
+ * times as long, here and in moe_q4_grouped. */
 moe_status moe_q4_linear(const moe_q4* q, const void* x, moe_dtype xt, int T, void* y, moe_dtype yt,
                          moe_stream_t stream);
 

@@ -8,9 +8,9 @@
 // Codes are converted where they are used: twice for the two halves of the rows, which
 // costs less than bf16 through LDS.
 //
-// Measured, 4096 rows of 32 experts, SWIGLU of 2048, 4096 inputs: MXFP4 195 to 205 us, 680
-// TFLOP/s (some 90 row tiles, a third of them short; 16384 rows 586 us, 938 TFLOP/s; a large
-// bf16 product 1170); integer codes in groups of 128 320 us, of 32 502, fp32 x 564.  Bound by
+// Measured, 4096 rows of 32 experts, SWIGLU of 2048, 4096 inputs: MXFP4 205 to 211 us, 650 to
+// 670 TFLOP/s (some 90 row tiles, a third of them short; 16384 rows 574 us, 958 TFLOP/s; a large
+// bf16 product 1170 to 1410); integer codes in groups of 128 315 us, of 32 501, fp32 x 549.  Bound by
 // the conversion of the codes, which leaves the matrix units waiting, then by the short tiles.
 #include "q4_dev.h"
 
@@ -387,9 +387,8 @@ struct TileKernel {
         }
         buf = buf == kRing - 1 ? 0 : buf + 1;
       };
-      // Rows end inside a stage only where a stage's groups may: kChunk counts its own, and
-      // kFold2 takes the last stage by itself.  The same for kStage would be dead code that
-      // spilled registers.
+      // Rows end inside a stage in two forms: kChunk counts its chunks, and kFold2 takes the last
+      // stage by itself.  Built for kStage too, which has none, that stage made registers spill.
       for (int s = 0; s < (MODE == kFold2 ? whole : stages); ++s) stage(std::true_type{}, s);
       if constexpr (MODE == kFold2) {
         if (whole < stages) stage(std::false_type{}, whole);

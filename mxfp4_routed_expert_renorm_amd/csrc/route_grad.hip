@@ -2,15 +2,16 @@
 // fixed (moe_route_grad).  With g the gradient of the weights w and m = sum g w / sum w
 // over the picks (renormalised weights; else 0):
 //   sigmoid  w (1 - s) (g - m) at the picks,   softmax, renormalised  w (g - m) at the picks,
-//   softmax  sum over e's picks of g w - s[e] sum g w  at every expert e.
+//   softmax  sum over e's picks of g w - s[e] sum g w  at every expert e, at picks as
+//            (1 - s[e]) (e's g w) - s[e] (the others' g w).
 // Dividing by sum w, not by the scale, makes m the weights' own mean: a part common to
 // all g cancels to the last bit however w was rounded.
 //
 // One wavefront per token: lane i holds pick i, and expert 4 (lane + 64 j) + i is
-// element i of a lane's vector j, so that a row leaves in 16-byte stores.
+// element i of a lane's vector j; elements are stored one by one, as rows start anywhere.
 //
-// Bound by the launch and a token's chain of loads, reductions and stores: 4096 tokens of
-// 256 experts 4.6 us, 777 of 300, every expert's gradient, 4.8 (1.9 a launch alone).
+// 4096 tokens of 256 experts 4.7 us, 777 of 300, every expert's gradient, 4.9: a launch
+// alone is 1.9, the rest a token's loads, reductions and stores, not measured apart.
 #include "chunk_dev.h"
 
 namespace moe {
